@@ -243,30 +243,32 @@ def _plain_tables(s):
     P = ring.numel()
     head, count = s["state"][0].long(), s["state"][1].long()
     ends, fresh = new < 0, new.clamp(min=0)
-    have = (ctx + page - 1) // page
-    seq = torch.where(ends, 0, ctx + fresh)
-    need = torch.where(ends, 0, ((seq + page - 1) // page).clamp(max=W) - have.clamp(max=W))
-    gives = torch.where(ends, have.clamp(max=W), 0)
-    first, gfirst = need.cumsum(0) - need, gives.cumsum(0) - gives
+    cu = torch.cat([fresh.new_zeros(1), fresh.cumsum(0)])
+    have, want = (ctx + page - 1) // page, (ctx + fresh + page - 1) // page
+    # a request gets all the pages that it needs, or it does not advance
+    fits = ~ends & (want <= W) & (cu[1:] <= tokens)
+    need = torch.where(fits, want - have, 0)
+    first = need.cumsum(0) - need
+    granted = fits & ((need == 0) | (first + need <= count))
+    need = torch.where(granted, need, 0)
+    seq = torch.where(ends, 0, torch.where(granted, ctx + fresh, ctx))
     # new pages, request by request, off the ring's head
     col = torch.arange(W, device=DEV)[None]
-    k = first[:, None] + col - have[:, None]
     takes = (col >= have[:, None]) & (col < (have + need)[:, None])
-    table.copy_(torch.where(takes, torch.where(k < count, ring[(head + k) % P], -1), table))
+    table.copy_(torch.where(takes, ring[(head + first[:, None] + col - have[:, None]) % P], table))
     # the pages of requests that end, to the ring's tail
+    gives = torch.where(ends, have.clamp(max=W), 0)
     back = ends[:, None] & (col < gives[:, None])
-    ring[((head + count + gfirst[:, None] + col) % P)[back]] = table[back]
+    ring[((head + count + (gives.cumsum(0) - gives)[:, None] + col) % P)[back]] = table[back]
     # the tokens
-    cu = torch.cat([fresh.new_zeros(1), fresh.cumsum(0)])
     t = torch.arange(tokens, device=DEV)
     b = torch.searchsorted(cu[1:], t, right=True).clamp(max=B - 1)
     live = t < cu[-1]
     pos = torch.where(live, ctx[b] + t - cu[b], 0)
     at = table[b, (pos // page).clamp(max=W - 1)].long()
-    slots = torch.where(live & (pos < W * page) & (at >= 0), at * page + pos % page, -1)
-    taken = torch.minimum(need.sum(), count)
-    lost = (((slots < 0) & live).sum() + (cu[-1] - tokens).clamp(min=0))
-    ring_state = torch.stack([(head + taken) % P, count - taken + gives.sum(), need.sum() - taken, lost])
+    slots = torch.where(live & granted[b] & (at >= 0), at * page + pos % page, -1)
+    taken, asked = need.sum(), torch.where(fits, want - have, 0).sum()
+    ring_state = torch.stack([(head + taken) % P, count - taken + gives.sum(), asked - taken, (~ends & ~granted).sum()])
     as32 = torch.int32
     return dict(seq_lens=seq.to(as32), cu_new=cu.to(as32), positions=pos.to(as32), slots=slots.to(as32), ring_state=ring_state.to(as32), table=table, ring=ring)
 
