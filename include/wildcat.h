@@ -25,7 +25,8 @@
  * --------------------------------
  *  - An "instance" is one (batch, head) pair; BH instances are independent
  *    and are stored one after another (instance b = batch * H + head).
- *  - All tensors are dense, row-major and contiguous.  Q is [BH, m, d];
+ *  - All tensors are dense, row-major and contiguous, unless strides are
+ *    given (the paged calls and wildcat_rotary).  Q is [BH, m, d];
  *    K and V are [BH, n, d]; their dtype is WILDCAT_F32 or WILDCAT_BF16.
  *    Every other tensor has a fixed type given below.
  *  - The factor F is float32 [BH, r, n]: F[b, i, l] is entry l of factor
@@ -43,7 +44,9 @@
  *    enqueued.  A failed launch returns WILDCAT_ERR_CUDA.  In every error
  *    case wildcat_last_error() (per thread) describes the failure.
  *  - Supported head dims: d in {32, 64, 128}.  Device pointers to Q, K, V,
- *    K_S must be 16-byte aligned.
+ *    K_S must be 16-byte aligned (the paged calls and wildcat_rotary take any
+ *    element-aligned pointer, and are faster where pointers and strides are
+ *    multiples of 16 bytes).
  *  - An instance whose pivots run out before r (total residual mass zero,
  *    or a pivot residual g_s <= eps, the truncation that stands in for the
  *    pseudo-inverse) has effective rank r' < r.  That is not an error: the
@@ -241,6 +244,135 @@ wildcat_status wildcat_decode_attend(const void* Q_new, const void* K_new, const
                                      float* O, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * An exact key / value cache in pages, beside the compressed one: for what is
+ * not compressed yet, or not at all.
+ *
+ *  - A pool holds `pages` pages of `page_size` rows for every key head; its
+ *    element strides are given as {page, head, row}, the d elements of a row
+ *    are contiguous.  Slot s is row s % page_size of page s / page_size.
+ *  - Request b's position x lies in page block_table[b * table_stride + x /
+ *    page_size] at row x % page_size.
+ *  - New tokens of all requests stand one after another: request b's are the
+ *    rows cu_new[b] .. cu_new[b + 1] - 1 of Q, k, v and O.  Strides of these
+ *    are element strides {token, head}.
+ *
+ * wildcat_page_tables -- positions, slots and pages of a step from the
+ * requests' lengths.  Request b has ctx_lens[b] cached tokens and new_lens[b]
+ * new ones; new_lens[b] < 0 says that it ends.  A request needs the pages
+ * ceil(ctx / page_size) .. ceil((ctx + new) / page_size) - 1 of its row; the
+ * k-th page needed (requests in order) is free_ring[(head + k) % P].  A request
+ * gets all of them or does not advance: its length stays, its tokens get slot
+ * -1, its row of the table is left as it is.  It does not advance when the ring
+ * has too few pages for it and all needs before it, when it needs more than W
+ * entries, or when its tokens run past max_tokens.  The ceil(ctx / page_size)
+ * pages of a request that ends go behind the ring's last page (to be handed out
+ * by later calls); its row is left as it is.
+ *
+ *   ctx_lens, new_lens  [B] int32, B <= 16384
+ *   block_table  in/out [B, W] int32, rows table_stride entries apart; only the
+ *                entries of pages handed out are written
+ *   free_ring    in/out [P] int32 page ids (P the pool's pages)
+ *   ring_state   [2] int32: place of the first free page in the ring, free pages
+ *   seq_lens     out [B] int32 lengths after the step (0 for a request that ends)
+ *   cu_new       out [B + 1] int32 new tokens before each request
+ *   positions, slots  out [max_tokens] int32; rows behind the last token get
+ *                position 0 and slot -1
+ *   ring_out     out [4] int32: the ring's state after the step (2 entries),
+ *                pages that were asked for and not there, requests that do not
+ *                advance
+ * An output must not share memory with an input.  The same inputs give the same
+ * outputs: ring_state is not changed in place.
+ */
+wildcat_status wildcat_page_tables(const int32_t* ctx_lens, const int32_t* new_lens, int64_t B,
+                                   int32_t* block_table, int64_t table_stride, int64_t W,
+                                   int32_t* free_ring, int64_t P, const int32_t* ring_state,
+                                   int page_size, int64_t max_tokens, int32_t* seq_lens,
+                                   int32_t* cu_new, int32_t* positions, int32_t* slots,
+                                   int32_t* ring_out, void* stream);
+
+/*
+ * wildcat_rotary -- rotary positions with several axes (time, height, width).
+ * Of each row of d elements the first 2 h, h = sum of sections, form h pairs:
+ * elements (i, i + h), or (2 i, 2 i + 1) with `interleaved`; the rest is copied.
+ * The first sections[0] pairs belong to axis 0, the next sections[1] to axis 1,
+ * and so on; pair i of axis a turns by angle positions[a][t] * inv_freq[i]:
+ *   (u, v) = (x cos - y sin, y cos + x sin).
+ * `backward` turns by minus the angle: the gradient of x from that of out.
+ * Angles are reduced in double; products and sums are float32, rounded once.
+ *
+ *   x          [T, H, d], dtype `dtype`, element strides x_token and x_head
+ *   positions  [axes][T] int32, axes pos_stride entries apart (axes <= 4)
+ *   inv_freq   [h] float64, radians per position
+ *   sections   HOST [axes] int32, sum h with 1 <= h <= d / 2
+ *   out        out [T, H, d]; may be x itself with the same strides
+ * d even, at most 1024.
+ */
+wildcat_status wildcat_rotary(const void* x, int64_t x_token, int64_t x_head, int dtype, int64_t T,
+                              int H, int d, const int32_t* positions, int64_t pos_stride,
+                              const double* inv_freq, const int32_t* sections, int axes,
+                              int interleaved, int backward, void* out, int64_t out_token,
+                              int64_t out_head, void* stream);
+
+/*
+ * wildcat_paged_write -- keys and values of new tokens into the cache, and with
+ * positions the rotary of keys and queries fused with it: row t of v and row t
+ * of k (turned as by wildcat_rotary when `positions` is not NULL) go to slot
+ * slots[t]; q_in, if not NULL, is turned into q_out.  Tokens with slot -1 are not
+ * written (their queries are).  A slot past the pool is not written and leaves
+ * WILDCAT_ERR_INVALID_ARG in the device status.  Two tokens of one call must not
+ * have the same slot.
+ *
+ *   k, v       [T, Hkv, d] with element strides {token, head}
+ *   slots      [T] int32
+ *   k_pool, v_pool  [pages, Hkv, page_size, d], HOST strides {page, head, row}
+ *   positions, pos_stride, inv_freq, sections, axes, interleaved   as above
+ *   q_in, q_out  [T, Hq, d]; q_out may be q_in itself with the same strides
+ */
+wildcat_status wildcat_paged_write(const void* k, int64_t k_token, int64_t k_head, const void* v,
+                                   int64_t v_token, int64_t v_head, const int32_t* slots, int dtype,
+                                   int64_t T, int Hkv, int d, void* k_pool, const int64_t* k_strides,
+                                   void* v_pool, const int64_t* v_strides, int64_t pages,
+                                   int page_size, const int32_t* positions, int64_t pos_stride,
+                                   const double* inv_freq, const int32_t* sections, int axes,
+                                   int interleaved, const void* q_in, int64_t q_token, int64_t q_head,
+                                   int Hq, void* q_out, int64_t q_out_token, int64_t q_out_head,
+                                   void* stream);
+
+/*
+ * wildcat_paged_attend -- exact attention of new tokens over the paged cache:
+ *   O_i = sum_{j < e_i} p_ij v_j / sum_{j < e_i} p_ij,  p_ij = exp(beta <q_i, k_j>),
+ *   e_i = L - n + i + 1 for token i of a request's n new ones (causal), else L,
+ * L = seq_lens[b] (the new tokens counted in when causal, their keys and values
+ * already in the cache).  Query head x reads key head x / (Hq / Hkv).  A row that
+ * sees no key is zero.  Rows of Q at or past cu_new[B] are not read, and those
+ * rows of O not written.  What the cache holds at positions at or past L does not
+ * matter (infinities and NaN included); a NaN or infinite key or value at a
+ * visible position of one row may reach the rows near it that do not see it.
+ * A page id outside the pool reads as zero keys and values, and a length past
+ * W * page_size is cut to it; both leave WILDCAT_ERR_INVALID_ARG in the device
+ * status.
+ *
+ *   Q      [T, Hq, d], dtype `dtype`, element strides q_token and q_head
+ *   k_pool, v_pool  [pages, Hkv, page_size, d], HOST strides {page, head, row}
+ *   seq_lens [B], cu_new [B + 1] int32, cu_new[0] = 0
+ *   beta   softmax scale (> 0, finite)
+ *   O      out [T, Hq, d], dtype `dtype`, element strides o_token and o_head
+ *   lse    out [T, Hq] float32 log of the sum of exponentials (-inf for rows that
+ *          see no key), or NULL
+ *   workspace >= wildcat_paged_attend_workspace_size(B, d) bytes; two calls that
+ *          may run at the same time need two of them
+ */
+size_t wildcat_paged_attend_workspace_size(int64_t B, int d);
+wildcat_status wildcat_paged_attend(const void* Q, int64_t q_token, int64_t q_head,
+                                    const void* k_pool, const int64_t* k_strides, const void* v_pool,
+                                    const int64_t* v_strides, int64_t pages, int page_size, int dtype,
+                                    int64_t T, int Hq, int Hkv, int d, const int32_t* block_table,
+                                    int64_t table_stride, int64_t W, const int32_t* seq_lens,
+                                    const int32_t* cu_new, int64_t B, float beta, int causal, void* O,
+                                    int64_t o_token, int64_t o_head, float* lse, void* workspace,
+                                    size_t ws_bytes, void* stream);
+
+/*
  * wildcat_attend_noalloc -- wildcat_attend for callers that cannot allocate
  * device memory.  The paper has no counterpart; this is a deployment
  * convenience.  Such callers only hold pointers handed to them by another
@@ -420,8 +552,10 @@ wildcat_status wildcat_pivot_uniforms(uint64_t seed, int64_t BH, int steps, doub
  * copies in flight, releases its tensor memory and returns, leaving its
  * output incomplete (the select stops every CTA of the instance at the same
  * step and reports the steps taken as the rank).
- * Returns WILDCAT_OK, WILDCAT_ERR_TIMEOUT, or WILDCAT_ERR_CUDA if the stream
- * or the status word could not be read.
+ * The paged calls record WILDCAT_ERR_INVALID_ARG there for slots, page ids and
+ * lengths in device memory that lie outside their tensors (such accesses are
+ * skipped).  Returns WILDCAT_OK, WILDCAT_ERR_TIMEOUT, WILDCAT_ERR_INVALID_ARG, or
+ * WILDCAT_ERR_CUDA if the stream or the status word could not be read.
  */
 wildcat_status wildcat_get_device_status(void* stream);
 

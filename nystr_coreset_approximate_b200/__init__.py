@@ -14,6 +14,13 @@ Method: "WildCat: Near-Linear Attention in Theory and Practice"
     V_S, w, vmin, vmax = weights(F, S, rank, V)             # Alg. 2 CompressKV
     O_hat = attend(Q, K_S, rank, beta, V_S, w, vmin, vmax)  # Alg. 3 WtdAttn
     O_hat, S, rank = forward(Q, K, V, beta, r, seed)        # Alg. 4 WildCat
+
+An exact cache in pages stands beside the compressed one, for keys and values
+that are not compressed yet, or not at all; one step of a serving program:
+
+    seq_lens, cu_new, positions, slots, ring = page_tables(ctx_lens, new_lens, ...)
+    q = paged_write(k, v, slots, k_pool, v_pool, q=q, positions=positions, ...)
+    O = paged_attend(q, k_pool, v_pool, block_table, seq_lens, cu_new, beta)
 """
 from __future__ import annotations
 
@@ -27,7 +34,7 @@ __all__ = [
     "weights", "weights_inverse", "attend", "attend_noalloc", "decode_attend", "forward", "forward_ex", "Options", "forward_binned", "BinnedForwardPlan", "forward_host", "ForwardPlan", "pivot_uniforms",
     "set_select_cluster", "last_select_cluster", "set_select_kernel", "last_select_kernel",
     "force_select_timeout", "last_select_threads", "set_select_phase_steps", "last_select_phases",
-    "set_stage_events",
+    "set_stage_events", "page_tables", "rotary", "rotary_backward", "paged_write", "paged_attend",
     "device_status", "DTYPES",
 ]
 
@@ -83,6 +90,17 @@ _SIGS = {
     "wildcat_forward_ex_host_workspace_size": ([_i64, _i64, _i64, _int, _int, _int, _vp], _sz),
     "wildcat_forward_ex_host": ([_vp, _vp, _vp, _int, _i64, _i64, _i64, _int, _f32, _int, _u64, _i64, _f32,
                                  _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
+    "wildcat_page_tables": ([_vp, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _int, _i64, _vp, _vp, _vp, _vp,
+                             _vp, _vp], _int),
+    "wildcat_rotary": ([_vp, _i64, _i64, _int, _i64, _int, _int, _vp, _i64, _vp, _vp, _int, _int, _int, _vp,
+                        _i64, _i64, _vp], _int),
+    "wildcat_paged_write": ([_vp, _i64, _i64, _vp, _i64, _i64, _vp, _int, _i64, _int, _int, _vp, _vp, _vp, _vp,
+                             _i64, _int, _vp, _i64, _vp, _vp, _int, _int, _vp, _i64, _i64, _int, _vp, _i64,
+                             _i64, _vp], _int),
+    "wildcat_paged_attend_workspace_size": ([_i64, _int], _sz),
+    "wildcat_paged_attend": ([_vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _int, _int, _i64, _int, _int, _int,
+                              _vp, _i64, _i64, _vp, _vp, _i64, _f32, _int, _vp, _i64, _i64, _vp, _vp, _sz,
+                              _vp], _int),
     "wildcat_pivot_uniforms": ([_u64, _i64, _int, _vp, _vp], _int),
     "wildcat_get_device_status": ([_vp], _int),
     "wildcat_test_force_wait_timeout": ([_i64], _int),
@@ -530,6 +548,225 @@ def forward_ex_host(Q_host, K_host, V_host, beta: float, r: int, seed: int = 0, 
     return O, S, rank
 
 
+# --------------------------------------------------------------------------- exact cache in pages
+def _rows(t, name, dims, dtype=None):
+    """Pointer of a strided CUDA tensor whose last dimension is contiguous."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    cur = _torch().cuda.current_device()
+    if t.device.index != cur:
+        raise ValueError(f"{name} is on cuda:{t.device.index} but the current device is cuda:{cur}; "
+                         f"call under torch.cuda.device({t.device.index})")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    return _vp(t.data_ptr())
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty on the stream that the call's kernels run on, so that the
+    allocator does not hand its memory on while they use it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _shape_is(t, name, *shape):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+
+
+def _pool(k_pool, v_pool):
+    """(pages, Hkv, page_size, d) of a pair of pools, and their strides {page, head, row}."""
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
+        raise ValueError("k_pool and v_pool must both be [pages, Hkv, page_size, d]")
+    if k_pool.dtype != v_pool.dtype:
+        raise TypeError("k_pool and v_pool must share a dtype")
+    return k_pool.shape, (_i64 * 3)(*k_pool.stride()[:3]), (_i64 * 3)(*v_pool.stride()[:3])
+
+
+def page_tables(ctx_lens, new_lens, block_table, free_ring, ring_state, page_size: int, max_tokens: int, *,
+                stream=None):
+    """Positions, slots and pages of a step from the requests' lengths (all
+    int32).  Request b has ctx_lens[b] cached tokens and new_lens[b] new ones
+    (-1: it ends).  New pages come off free_ring [P] at ring_state = (first
+    free place, free pages) and go into block_table [B, W]; pages of requests
+    that end go back to the ring; both tensors are updated in place.  A
+    request gets all the pages it needs or does not advance.
+
+    Returns (seq_lens [B], cu_new [B + 1], positions [max_tokens],
+    slots [max_tokens], ring_out [4]): ring_out[:2] is the next call's
+    ring_state, ring_out[2] the pages that were missing and ring_out[3] the
+    requests that did not advance."""
+    torch = _torch()
+    i32 = torch.int32
+    B = ctx_lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, W]")
+    _shape_is(new_lens, "new_lens", B)
+    if ring_state.numel() < 2:
+        raise ValueError("ring_state must hold (first free place, free pages)")
+    if max_tokens < 0:
+        raise ValueError("max_tokens must be >= 0")
+    W = block_table.shape[1]
+    # one allocation for the five outputs (each begins on a 16-byte boundary)
+    sizes = [B, B + 1, max_tokens, max_tokens, 4]
+    flat = _empty(sum(-(-n // 4) * 4 for n in sizes), i32, ctx_lens.device, stream)
+    outs, at = [], 0
+    for n in sizes:
+        outs.append(flat[at:at + n])
+        at += -(-n // 4) * 4
+    seq_lens, cu_new, positions, slots, ring_out = outs
+    _check(lib().wildcat_page_tables(
+        _dev(ctx_lens, "ctx_lens", i32), _dev(new_lens, "new_lens", i32), B, _rows(block_table, "block_table", 2, i32),
+        block_table.stride(0) if B > 1 else max(W, 1), W, _dev(free_ring, "free_ring", i32), free_ring.numel(),
+        _dev(ring_state, "ring_state", i32), int(page_size), int(max_tokens), _dev(seq_lens, "seq_lens"),
+        _dev(cu_new, "cu_new"), _dev(positions, "positions"), _dev(slots, "slots"), _dev(ring_out, "ring_out"),
+        _stream(stream)))
+    return seq_lens, cu_new, positions, slots, ring_out
+
+
+def _turn_args(positions, inv_freq, sections, T, d):
+    """(positions pointer, axis stride, inv_freq pointer, sections, axes) of the rotary calls."""
+    torch = _torch()
+    sections = [int(s) for s in sections]
+    if positions.dim() == 1:
+        positions = positions[None]
+    if positions.dim() != 2 or positions.shape[1] != T:
+        raise ValueError("positions must be [axes, T], or [T] for one axis")
+    if positions.shape[0] != len(sections):
+        raise ValueError("sections must name the pairs of each axis of positions")
+    half = sum(sections)
+    if inv_freq.dim() != 1 or inv_freq.shape[0] != half:
+        raise ValueError(f"inv_freq must hold one frequency for each of the {half} pairs")
+    return (_rows(positions, "positions", 2, torch.int32), positions.stride(0), _dev(inv_freq, "inv_freq", torch.float64),
+            (_int * max(1, len(sections)))(*sections), len(sections))
+
+
+def _rotary(x, positions, inv_freq, sections, interleaved, backward, out, stream, name):
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [T, H, d]")
+    T, H, d = x.shape
+    code = _dtype_code(x)
+    if out is None:
+        out = _empty((T, H, d), x.dtype, x.device, stream)
+    _shape_is(out, "out", T, H, d)
+    pos, pos_stride, freq, secs, axes = _turn_args(positions, inv_freq, sections, T, d)
+    _check(lib().wildcat_rotary(_rows(x, name, 3), x.stride(0), x.stride(1), code, T, H, d, pos, pos_stride, freq,
+                                secs, axes, int(bool(interleaved)), backward, _rows(out, "out", 3, x.dtype),
+                                out.stride(0), out.stride(1), _stream(stream)))
+    return out
+
+
+def rotary(x, positions, inv_freq, sections, *, interleaved: bool = False, out=None, stream=None):
+    """Rotary positions with several axes.  x [T, H, d] (float32 or bfloat16,
+    strided); positions [axes, T] int32 ([T] for one axis); inv_freq [h]
+    float64 radians per position; sections: the pairs of each axis, summing to
+    h <= d / 2.  Pair i is elements (i, i + h), or (2 i, 2 i + 1) when
+    interleaved; elements past 2 h are copied.  For Q or K [BH, n, d] with one
+    grid of positions, pass Q.transpose(0, 1).  out may be x itself."""
+    return _rotary(x, positions, inv_freq, sections, interleaved, 0, out, stream, "x")
+
+
+def rotary_backward(grad_out, positions, inv_freq, sections, *, interleaved: bool = False, out=None, stream=None):
+    """The gradient of rotary's x from that of its result: the turn by minus
+    the angle."""
+    return _rotary(grad_out, positions, inv_freq, sections, interleaved, 1, out, stream, "grad_out")
+
+
+def paged_write(k, v, slots, k_pool, v_pool, *, q=None, positions=None, inv_freq=None, sections=None,
+                interleaved: bool = False, out=None, stream=None):
+    """Rows of k and v [T, Hkv, d] into the pools [pages, Hkv, page_size, d] at
+    slots [T] int32 (-1: not written).  With positions, inv_freq and sections
+    (as for rotary) the keys are turned on the way, and the queries q
+    [T, Hq, d], if given, beside them: their turned form is returned (in
+    `out`, which may be q).  Returns None without q."""
+    torch = _torch()
+    if k.dim() != 3 or k.shape != v.shape:
+        raise ValueError("k and v must both be [T, Hkv, d]")
+    T, Hkv, d = k.shape
+    (pages, heads, page_size, pd), ks, vs = _pool(k_pool, v_pool)
+    if (heads, pd) != (Hkv, d):
+        raise ValueError("k and the pools must have the same heads and head dim")
+    if not k.dtype == v.dtype == k_pool.dtype:
+        raise TypeError("k, v and the pools must share a dtype")
+    _shape_is(slots, "slots", T)
+    pos = freq = secs = None
+    pos_stride = axes = Hq = qt = qh = ot = oh = 0
+    qp = op = None
+    if positions is not None:
+        if inv_freq is None or sections is None:
+            raise ValueError("positions need inv_freq and sections")
+        pos, pos_stride, freq, secs, axes = _turn_args(positions, inv_freq, sections, T, d)
+    if q is not None:
+        if positions is None:
+            raise ValueError("q is turned by positions: give them, or leave q out")
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d:
+            raise ValueError("q must be [T, Hq, d]")
+        Hq = q.shape[1]
+        if out is None:
+            out = _empty((T, Hq, d), q.dtype, q.device, stream)
+        _shape_is(out, "out", T, Hq, d)
+        qp, op = _rows(q, "q", 3, k.dtype), _rows(out, "out", 3, k.dtype)
+        qt, qh, ot, oh = q.stride(0), q.stride(1), out.stride(0), out.stride(1)
+    elif out is not None:
+        raise ValueError("out without q")
+    _check(lib().wildcat_paged_write(
+        _rows(k, "k", 3), k.stride(0), k.stride(1), _rows(v, "v", 3), v.stride(0), v.stride(1),
+        _dev(slots, "slots", torch.int32), _dtype_code(k), T, Hkv, d, _rows(k_pool, "k_pool", 4), ks,
+        _rows(v_pool, "v_pool", 4), vs, pages, page_size, pos, pos_stride, freq, secs, axes, int(bool(interleaved)),
+        qp, qt, qh, Hq, op, ot, oh, _stream(stream)))
+    return out
+
+
+def paged_attend(q, k_pool, v_pool, block_table, seq_lens, cu_new, beta: float, *, causal: bool = True, lse=None,
+                 out=None, stream=None):
+    """Exact attention of new tokens over the paged cache.  q [T, Hq, d]
+    (float32 or bfloat16, strided): request b's tokens are rows
+    cu_new[b] .. cu_new[b + 1]; its keys are the first seq_lens[b] positions
+    of its pages block_table[b].  causal: token i of n sees the first
+    seq_lens[b] - n + i + 1 of them, else all see all (an encoder's states).
+    Hq is a multiple of the pools' heads.  A row that sees no key is zero.
+    Returns O [T, Hq, d] in q's dtype (rows at or past cu_new[B] are not
+    written); lse, a float32 [T, Hq] tensor, receives the logs of the sums of
+    exponentials."""
+    torch = _torch()
+    i32 = torch.int32
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, d]")
+    T, Hq, d = q.shape
+    (pages, Hkv, page_size, pd), ks, vs = _pool(k_pool, v_pool)
+    if pd != d:
+        raise ValueError("q and the pools must have the same head dim")
+    if q.dtype != k_pool.dtype:
+        raise TypeError("q and the pools must share a dtype")
+    B = seq_lens.shape[0]
+    _shape_is(cu_new, "cu_new", B + 1)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, W]")
+    if out is None:
+        out = _empty((T, Hq, d), q.dtype, q.device, stream)
+    _shape_is(out, "out", T, Hq, d)
+    if lse is not None:
+        _shape_is(lse, "lse", T, Hq)
+    L = lib()
+    W = block_table.shape[1]
+    nbytes = int(L.wildcat_paged_attend_workspace_size(B, d))
+    ws = _empty(nbytes, torch.uint8, q.device, stream)
+    _check(L.wildcat_paged_attend(
+        _rows(q, "q", 3), q.stride(0), q.stride(1), _rows(k_pool, "k_pool", 4), ks, _rows(v_pool, "v_pool", 4), vs,
+        pages, page_size, _dtype_code(q), T, Hq, Hkv, d, _rows(block_table, "block_table", 2, i32),
+        block_table.stride(0) if B > 1 else max(W, 1), W, _dev(seq_lens, "seq_lens", i32), _dev(cu_new, "cu_new", i32),
+        B, float(beta), int(bool(causal)), _rows(out, "out", 3, q.dtype), out.stride(0), out.stride(1),
+        _opt(lse, "lse", torch.float32), _dev(ws, "workspace"), nbytes, _stream(stream)))
+    return out
+
+
 def pivot_uniforms(seed: int, BH: int, steps: int, device="cuda"):
     """The pivot uniforms u[b, i] the select kernels draw (float64, device)."""
     torch = _torch()
@@ -541,7 +778,8 @@ def pivot_uniforms(seed: int, BH: int, steps: int, device="cuda"):
 
 def device_status(stream=None) -> int:
     """Wait for the stream, then return and clear the device status word
-    (0 = fine, 5 = a kernel's bounded wait expired)."""
+    (0 = fine, 1 = a paged call met a slot, page id or length outside its
+    tensor, 5 = a kernel's bounded wait expired)."""
     return int(lib().wildcat_get_device_status(_stream(stream)))
 
 

@@ -344,12 +344,13 @@ Status stage_host_inputs(HostPipe* hp, cudaStream_t s, void* Kd, void* Vd, void*
 
 namespace wildcat {
 int read_device_status(bool clear) {
-    const int parts[3] = {read_attend_status(clear), read_weights_status(clear), read_select_gs_status(clear)};
+    const int parts[] = {read_attend_status(clear), read_weights_status(clear), read_select_gs_status(clear),
+                         read_paged_status(clear), read_paged_attend_status(clear)};
     for (const int v : parts)
         if (v < 0) return -1;
-    for (const int v : parts)
-        if (v) return v;
-    return 0;
+    int worst = 0;  // an expired wait (5) before a bad slot, page id or length (1)
+    for (const int v : parts) worst = v > worst ? v : worst;
+    return worst;
 }
 }  // namespace wildcat
 
@@ -805,6 +806,8 @@ wildcat_status wildcat_get_device_status(void* stream) {
     const int v = wildcat::read_device_status(true);
     if (v < 0) return record(Status::fail(3, "wildcat_get_device_status: cannot read the status word"));
     if (v == WILDCAT_ERR_TIMEOUT) return record(Status::fail(5, "a kernel's bounded wait expired"));
+    if (v == WILDCAT_ERR_INVALID_ARG)
+        return record(Status::fail(1, "a kernel met a slot, page id or length outside its tensor"));
     return record(Status::ok());
 }
 
@@ -856,5 +859,218 @@ wildcat_status wildcat_set_select_cluster(int ctas_per_instance) {
 }
 
 int wildcat_last_select_cluster(void) { return wildcat::last_select_cluster(); }
+
+}  // extern "C"
+
+extern "C" {
+
+wildcat_status wildcat_page_tables(const int32_t* ctx_lens, const int32_t* new_lens, int64_t B, int32_t* block_table,
+                                   int64_t table_stride, int64_t W, int32_t* free_ring, int64_t P,
+                                   const int32_t* ring_state, int page_size, int64_t max_tokens, int32_t* seq_lens,
+                                   int32_t* cu_new, int32_t* positions, int32_t* slots, int32_t* ring_out,
+                                   void* stream) {
+    const char* who = "wildcat_page_tables";
+    if (B < 0 || W < 0 || max_tokens < 0) return bad(1, "%s: B, W and max_tokens must be >= 0", who);
+    if (B > 16384) return bad(2, "%s: more than 16384 requests are not supported", who);
+    if (page_size < 1) return bad(1, "%s: page_size must be >= 1", who);
+    if (P < 1) return bad(1, "%s: the ring must hold at least one page", who);
+    if (table_stride < W) return bad(1, "%s: table_stride must be >= W", who);
+    if (P > 0x7fffffffLL || P * (int64_t)page_size > 0x7fffffffLL)
+        return bad(2, "%s: 2^31 or more slots are not supported", who);
+    if (max_tokens > 0x7fffffffLL || W > 0x7fffffffLL || B * W > 0x7fffffffLL)
+        return bad(2, "%s: 2^31 or more tokens or table entries are not supported", who);
+    if (!free_ring || !ring_state || !cu_new || !ring_out || (B > 0 && (!ctx_lens || !new_lens || !seq_lens)) ||
+        (B > 0 && W > 0 && !block_table) || (max_tokens > 0 && (!positions || !slots)))
+        return bad(1, "%s: null pointer argument", who);
+    if ((B > 0 && (seq_lens == ctx_lens || seq_lens == new_lens || block_table == free_ring)) || ring_out == ring_state)
+        return bad(1, "%s: an output must not be one of the inputs", who);
+    wildcat::TablesRequest q{ctx_lens, new_lens, B, block_table, table_stride, W, free_ring, P, ring_state, page_size,
+                             max_tokens, seq_lens, cu_new, positions, slots, ring_out};
+    return record(wildcat::launch_page_tables(q, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// The rotary arguments shared by wildcat_rotary and wildcat_paged_write.
+wildcat_status check_turn(wildcat::TurnRequest& q, int dtype, int64_t T, int d, const int32_t* positions,
+                          int64_t pos_stride, const double* inv_freq, const int32_t* sections, int axes,
+                          int interleaved, bool turns, const char* who) {
+    if (dtype != WILDCAT_F32 && dtype != WILDCAT_BF16) return bad(1, "%s: dtype must be WILDCAT_F32 or WILDCAT_BF16", who);
+    if (T < 0) return bad(1, "%s: T must be >= 0", who);
+    if (T > 0x7fffffffLL) return bad(2, "%s: 2^31 or more tokens are not supported", who);
+    if (d < 2 || d % 2 || d > 1024) return bad(2, "%s: head dim must be even, 2 to 1024", who);
+    q.dtype = dtype;
+    q.d = d;
+    q.T = T;
+    q.half = 0;
+    for (int a = 0; a < 4; ++a) q.ends[a] = 0;
+    if (!turns) return WILDCAT_OK;
+    if (axes < 1 || axes > 4) return bad(1, "%s: 1 to 4 axes", who);
+    if (!sections) return bad(1, "%s: sections must be non-null", who);
+    int64_t half = 0;
+    for (int a = 0; a < 4; ++a) {
+        if (a < axes) {
+            if (sections[a] < 0) return bad(1, "%s: sections must be >= 0", who);
+            half += sections[a];
+        }
+        q.ends[a] = (int)(half < 0x7fffffff ? half : 0x7fffffff);
+    }
+    if (half < 1 || 2 * half > d) return bad(1, "%s: the sections must sum to 1 .. d / 2 pairs", who);
+    if (T > 0 && (!positions || !inv_freq)) return bad(1, "%s: positions and inv_freq must be non-null", who);
+    if (pos_stride < 0) return bad(1, "%s: strides must be >= 0", who);
+    q.half = (int)half;
+    q.interleaved = interleaved != 0;
+    q.positions = positions;
+    q.pos_stride = pos_stride;
+    q.inv_freq = inv_freq;
+    return WILDCAT_OK;
+}
+
+bool elem_aligned(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % elem_bytes(dtype) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+wildcat_status wildcat_rotary(const void* x, int64_t x_token, int64_t x_head, int dtype, int64_t T, int H, int d,
+                              const int32_t* positions, int64_t pos_stride, const double* inv_freq,
+                              const int32_t* sections, int axes, int interleaved, int backward, void* out,
+                              int64_t out_token, int64_t out_head, void* stream) {
+    const char* who = "wildcat_rotary";
+    wildcat::TurnRequest q{};
+    wildcat_status st = check_turn(q, dtype, T, d, positions, pos_stride, inv_freq, sections, axes, interleaved, true, who);
+    if (st != WILDCAT_OK) return st;
+    if (H < 0) return bad(1, "%s: H must be >= 0", who);
+    if (H > 65535) return bad(2, "%s: more than 65535 heads are not supported", who);
+    if (T == 0 || H == 0) return record(Status::ok());
+    if (!x || !out) return bad(1, "%s: null pointer argument", who);
+    if (x_token < 0 || x_head < 0) return bad(1, "%s: strides must be >= 0", who);
+    if ((T > 1 && out_token < d) || (H > 1 && out_head < d)) return bad(1, "%s: rows of out overlap", who);
+    if (!elem_aligned(x, dtype) || !elem_aligned(out, dtype)) return bad(1, "%s: x and out must be aligned to their elements", who);
+    if (x == out && ((T > 1 && x_token != out_token) || (H > 1 && x_head != out_head)))
+        return bad(1, "%s: in place, x and out must have the same strides", who);
+    q.back = backward != 0;
+    q.part[0].src = x;
+    q.part[0].dst = out;
+    q.part[0].heads = H;
+    q.part[0].turn = true;
+    q.part[0].src_t = x_token;
+    q.part[0].src_h = x_head;
+    q.part[0].dst_t = out_token;
+    q.part[0].dst_h = out_head;
+    return record(wildcat::launch_turn(q, static_cast<cudaStream_t>(stream)));
+}
+
+wildcat_status wildcat_paged_write(const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                                   int64_t v_head, const int32_t* slots, int dtype, int64_t T, int Hkv, int d,
+                                   void* k_pool, const int64_t* k_strides, void* v_pool, const int64_t* v_strides,
+                                   int64_t pages, int page_size, const int32_t* positions, int64_t pos_stride,
+                                   const double* inv_freq, const int32_t* sections, int axes, int interleaved,
+                                   const void* q_in, int64_t q_token, int64_t q_head, int Hq, void* q_out,
+                                   int64_t q_out_token, int64_t q_out_head, void* stream) {
+    const char* who = "wildcat_paged_write";
+    wildcat::TurnRequest q{};
+    const bool turns = positions != nullptr;
+    wildcat_status st = check_turn(q, dtype, T, d, positions, pos_stride, inv_freq, sections, axes, interleaved, turns, who);
+    if (st != WILDCAT_OK) return st;
+    if (Hkv < 1 || pages < 0 || page_size < 1 || Hq < 0) return bad(1, "%s: Hkv and page_size must be >= 1, pages and Hq >= 0", who);
+    if (Hkv > 65535 || Hq > 65535) return bad(2, "%s: more than 65535 heads are not supported", who);
+    if (pages > 0x7fffffffLL || pages * (int64_t)page_size > 0x7fffffffLL)
+        return bad(2, "%s: 2^31 or more slots are not supported", who);
+    if (q_in && !turns) return bad(1, "%s: queries are written only where positions are given", who);
+    if (T == 0) return record(Status::ok());
+    if (!k || !v || !slots || !k_strides || !v_strides || (pages > 0 && (!k_pool || !v_pool)) || (q_in && !q_out))
+        return bad(1, "%s: null pointer argument", who);
+    if (k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0 || (q_in && (q_token < 0 || q_head < 0)))
+        return bad(1, "%s: strides must be >= 0", who);
+    for (const int64_t* s : {k_strides, v_strides})
+        if ((pages > 1 && s[0] < d) || (Hkv > 1 && s[1] < d) || (page_size > 1 && s[2] < d))
+            return bad(1, "%s: rows of a pool overlap", who);
+    if (q_in && ((T > 1 && q_out_token < d) || (Hq > 1 && q_out_head < d))) return bad(1, "%s: rows of q_out overlap", who);
+    if (q_in && q_in == q_out && ((T > 1 && q_token != q_out_token) || (Hq > 1 && q_head != q_out_head)))
+        return bad(1, "%s: in place, q and q_out must have the same strides", who);
+    for (const void* p : {k, v, (const void*)k_pool, (const void*)v_pool, q_in, (const void*)q_out})
+        if (!elem_aligned(p, dtype)) return bad(1, "%s: tensors must be aligned to their elements", who);
+    q.slots = slots;
+    q.pages = pages;
+    q.page_size = page_size;
+    const void* src[2] = {k, v};
+    void* dst[2] = {k_pool, v_pool};
+    const int64_t tok[2] = {k_token, v_token}, head[2] = {k_head, v_head};
+    for (int i = 0; i < 2; ++i) {
+        wildcat::TurnPart& p = q.part[i];
+        const int64_t* s = i ? v_strides : k_strides;
+        p.src = src[i];
+        p.dst = dst[i];
+        p.heads = Hkv;
+        p.turn = turns && i == 0;
+        p.pool = true;
+        p.src_t = tok[i];
+        p.src_h = head[i];
+        p.dst_t = s[0];
+        p.dst_h = s[1];
+        p.dst_r = s[2];
+    }
+    if (q_in && Hq > 0) {
+        wildcat::TurnPart& p = q.part[2];
+        p.src = q_in;
+        p.dst = q_out;
+        p.heads = Hq;
+        p.turn = true;
+        p.src_t = q_token;
+        p.src_h = q_head;
+        p.dst_t = q_out_token;
+        p.dst_h = q_out_head;
+    }
+    return record(wildcat::launch_turn(q, static_cast<cudaStream_t>(stream)));
+}
+
+size_t wildcat_paged_attend_workspace_size(int64_t B, int d) {
+    if (B < 0 || d < 1) return 0;
+    return wildcat::paged_attend_workspace_bytes(B, d);
+}
+
+wildcat_status wildcat_paged_attend(const void* Q, int64_t q_token, int64_t q_head, const void* k_pool,
+                                    const int64_t* k_strides, const void* v_pool, const int64_t* v_strides,
+                                    int64_t pages, int page_size, int dtype, int64_t T, int Hq, int Hkv, int d,
+                                    const int32_t* block_table, int64_t table_stride, int64_t W,
+                                    const int32_t* seq_lens, const int32_t* cu_new, int64_t B, float beta, int causal,
+                                    void* O, int64_t o_token, int64_t o_head, float* lse, void* workspace,
+                                    size_t ws_bytes, void* stream) {
+    const char* who = "wildcat_paged_attend";
+    if (dtype != WILDCAT_F32 && dtype != WILDCAT_BF16) return bad(1, "%s: dtype must be WILDCAT_F32 or WILDCAT_BF16", who);
+    if (d != 32 && d != 64 && d != 128) return bad(2, "%s: head dim must be 32, 64 or 128", who);
+    wildcat_status st = check_scalars(beta, 0.f, who);
+    if (st != WILDCAT_OK) return st;
+    if (B < 0 || T < 0 || W < 0 || pages < 0 || page_size < 1) return bad(1, "%s: B, T, W and pages must be >= 0, page_size >= 1", who);
+    if (Hkv < 1 || Hq < 1 || Hq % Hkv) return bad(1, "%s: Hq must be a multiple of Hkv, both >= 1", who);
+    if (B > 65535) return bad(2, "%s: B above 65535 is not supported", who);
+    if (Hq > 65535) return bad(2, "%s: more than 65535 heads are not supported", who);
+    if (pages > 0x7fffffffLL || pages * (int64_t)page_size > 0x7fffffffLL)
+        return bad(2, "%s: 2^31 or more slots are not supported", who);
+    if (T > 0x7fffffffLL || T * Hq > 0x7fffffffLL) return bad(2, "%s: 2^31 or more query rows are not supported", who);
+    if (W > 0x7fffffffLL) return bad(2, "%s: 2^31 or more table entries are not supported", who);
+    if (table_stride < W) return bad(1, "%s: table_stride must be >= W", who);
+    if (B == 0 || T == 0) return record(Status::ok());
+    if (!Q || !O || !k_strides || !v_strides || !seq_lens || !cu_new || !workspace || (W > 0 && !block_table) ||
+        (pages > 0 && (!k_pool || !v_pool)))
+        return bad(1, "%s: null pointer argument", who);
+    if (q_token < 0 || q_head < 0) return bad(1, "%s: strides must be >= 0", who);
+    for (const int64_t* s : {k_strides, v_strides})
+        for (int i = 0; i < 3; ++i)
+            if (s[i] < 0) return bad(1, "%s: strides must be >= 0", who);
+    if ((T > 1 && o_token < d) || (Hq > 1 && o_head < d)) return bad(1, "%s: rows of O overlap", who);
+    for (const void* p : {Q, k_pool, v_pool, (const void*)O})
+        if (!elem_aligned(p, dtype)) return bad(1, "%s: tensors must be aligned to their elements", who);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return bad(4, "%s: workspace must be 256-byte aligned", who);
+    if (ws_bytes < wildcat::paged_attend_workspace_bytes(B, d)) return bad(4, "%s: workspace too small", who);
+    wildcat::PagedAttendRequest q{Q, q_token, q_head, k_pool, v_pool, pages, page_size, k_strides[0], k_strides[1],
+                                  k_strides[2], v_strides[0], v_strides[1], v_strides[2], dtype, T, Hq, Hkv, d,
+                                  block_table, table_stride, W, seq_lens, cu_new, B, beta, causal != 0, O, o_token,
+                                  o_head, lse, workspace, ws_bytes};
+    return record(wildcat::launch_paged_attend(q, static_cast<cudaStream_t>(stream)));
+}
 
 }  // extern "C"

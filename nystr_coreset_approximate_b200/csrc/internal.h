@@ -173,6 +173,84 @@ struct DecodeRequest {
 size_t decode_workspace_bytes(int64_t BH, int d);
 Status launch_decode(const DecodeRequest& q, cudaStream_t stream);
 
+// ---- exact cache in pages (paged_cache.cu, paged_attend.cu, paged_attend_tc.cu) ----
+struct TablesRequest {
+    const int32_t* ctx_lens;
+    const int32_t* new_lens;
+    int64_t B;
+    int32_t* table;
+    int64_t table_stride, W;  // entries from one request's row to the next, entries of a row
+    int32_t* ring;
+    int64_t P;
+    const int32_t* ring_state;
+    int page_size;
+    int64_t max_tokens;
+    int32_t* seq_lens;
+    int32_t* cu_new;
+    int32_t* positions;
+    int32_t* slots;
+    int32_t* ring_out;
+};
+Status launch_page_tables(const TablesRequest& q, cudaStream_t stream);
+
+// One tensor of a rotary or write launch: rows of `heads` heads per token, read
+// from src and written to dst (strides in elements), rotated or copied; `pool`:
+// dst is a page pool (dst_t page stride, dst_h head stride, dst_r row stride).
+struct TurnPart {
+    const void* src = nullptr;
+    void* dst = nullptr;
+    int heads = 0;
+    bool turn = false, pool = false;
+    int64_t src_t = 0, src_h = 0, dst_t = 0, dst_h = 0, dst_r = 0;
+};
+struct TurnRequest {
+    int dtype, d;
+    int64_t T;
+    int half;      // rotated pairs of a head (0: nothing is rotated)
+    int ends[4];   // pair i belongs to the first axis a with i < ends[a]
+    bool interleaved, back;
+    const int32_t* positions;
+    int64_t pos_stride;
+    const double* inv_freq;
+    const int32_t* slots;
+    int64_t pages;
+    int page_size;
+    TurnPart part[3];
+};
+Status launch_turn(const TurnRequest& q, cudaStream_t stream);
+
+struct PagedAttendRequest {
+    const void* Q;
+    int64_t q_t, q_h;  // strides in elements: token, head
+    const void* K;
+    const void* V;
+    int64_t pages;
+    int page_size;
+    int64_t k_p, k_h, k_r, v_p, v_h, v_r;  // page, head and row strides in elements
+    int dtype;
+    int64_t T;
+    int Hq, Hkv, d;
+    const int32_t* table;
+    int64_t table_stride, W;
+    const int32_t* seq_lens;
+    const int32_t* cu_new;
+    int64_t B;
+    float beta;
+    bool causal;
+    void* O;
+    int64_t o_t, o_h;
+    float* lse;
+    void* ws;
+    size_t ws_bytes;
+};
+size_t paged_attend_workspace_bytes(int64_t B, int d);
+Status launch_paged_attend(const PagedAttendRequest& q, cudaStream_t stream);
+bool paged_attend_tc_supported(const PagedAttendRequest& q);
+Status launch_paged_attend_tc(const PagedAttendRequest& q, cudaStream_t stream);
+int read_paged_status(bool clear);
+int read_paged_attend_status(bool clear);
+int read_paged_attend_tc_status(bool clear);
+
 // per-instance key mean (binning.cu), fp64 partial sums then fp32 mean
 size_t key_mean_workspace_bytes(int64_t BH, int64_t n, int d);
 Status launch_key_mean(const void* K, int dtype, int64_t BH, int64_t n, int d, void* ws, float* kbar,

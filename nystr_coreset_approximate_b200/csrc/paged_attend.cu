@@ -1,0 +1,344 @@
+// paged_attend.cu -- exact attention of new tokens over a paged cache.
+//
+//   O_i = sum_{j < e_i} exp(beta <q_i, k_j>) v_j / sum_{j < e_i} exp(beta <q_i, k_j>),
+// e_i = L - n + i + 1 for token i of a request's n new ones (causal) or L; key
+// j lies in page table[j / page] at row j % page.  A row that sees no key is
+// zero (its log-sum -inf).  One pass over the keys with the running maximum m
+// and sum l of each row: when m grows to m', l and the accumulated values are
+// multiplied by 2^(m - m') (m in powers of two, beta log2(e) folded into the
+// scores).
+//
+// Here: the plan and the join (paged.cuh) that the tensor-core kernel of
+// paged_attend_tc.cu uses too, the dispatch, and the CUDA-core kernel, for
+// float32 and for bf16 in shapes that the tensor cores' copies do not take
+// (d = 32, a page that is no multiple of 8 rows, strides that are no multiple
+// of 16 bytes).  It works in float32 throughout: one row tile is 64 rows, or 16
+// where the unit has no more (a decoded token), against 64 keys; a thread holds
+// 4 x 4 (1 x 4) scores and 4 (1) rows of D / 16 accumulators.
+#include <algorithm>
+#include <cfloat>
+
+#include "common.cuh"
+#include "internal.h"
+#include "paged.cuh"
+#include "tc_common.cuh"
+
+namespace wildcat {
+
+__device__ int g_paged_attend_status = 0;  // WILDCAT_ERR_INVALID_ARG: lengths or page ids out of range
+
+namespace {
+
+using namespace paged;
+
+constexpr int kM = 64, kN = 64, kThreads = 256;
+constexpr int kPlanThreads = 512;
+constexpr int kPad = 4;
+
+int paged_sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 148;
+    }
+    return n;
+}
+
+struct SimtArgs {
+    Shape s;
+    Plan p;
+    const void* Q;
+    const void* K;
+    const void* V;
+    int64_t q_t, q_h, k_p, k_h, k_r, v_p, v_h, v_r, o_t, o_h;
+    void* O;
+    float* lse;
+    float scale;  // beta log2(e)
+    bool wide;    // 16-byte loads of Q, K and V
+    int G;
+};
+
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, bool wide, float (&v)[4]);
+template <>
+__device__ __forceinline__ void load4<float>(const float* p, bool wide, float (&v)[4]) {
+    if (wide) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = __ldg(p + k);
+    }
+}
+template <>
+__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, bool wide, float (&v)[4]) {
+    if (wide) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        v[0] = __uint_as_float(u.x << 16);
+        v[1] = __uint_as_float(u.x & 0xffff0000u);
+        v[2] = __uint_as_float(u.y << 16);
+        v[3] = __uint_as_float(u.y & 0xffff0000u);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = __bfloat162float(p[k]);
+    }
+}
+
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// 64 key (or value) rows from key k0 on into shared memory, widened; rows at or
+// past the length, or in a page outside the pool, as zeros.
+template <typename E, int D>
+__device__ __forceinline__ void load_rows(const SimtArgs& a, const Seg& g, const void* pool, int64_t sp, int64_t sh,
+                                          int64_t sr, int k0, float* dst) {
+    using T = typename E::T;
+    const T* base = static_cast<const T*>(pool) + (int64_t)g.h * sh;
+    const int32_t* tab = a.s.table + (int64_t)g.b * a.s.table_stride;
+    for (int e = threadIdx.x; e < kN * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c = (e - r * (D / 4)) * 4, j = k0 + r;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (j < g.L) {
+            const int p = j / a.s.page_size, id = tab[p];
+            if (id >= 0 && id < a.s.pages)
+                load4<T>(base + (int64_t)id * sp + (int64_t)(j - p * a.s.page_size) * sr + c, a.wide, v);
+            else
+                atomicExch(&g_paged_attend_status, 1);
+        }
+        *reinterpret_cast<float4*>(dst + r * (D + kPad) + c) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+// One segment with row tiles of 16 RT rows.
+template <typename E, int D, int RT>
+__device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* KVs, float* Ps) {
+    using T = typename E::T;
+    constexpr int MR = 16 * RT, CH = D / 64 > 0 ? D / 64 : 1, CW = D >= 64 ? 4 : 2;
+    constexpr int QS = D + kPad, PS = kN + kPad;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int first = a.s.first_row(g.b);
+    __syncthreads();  // the previous segment's reads are done
+    for (int e = tid; e < MR * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c = (e - r * (D / 4)) * 4;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r < g.rows) {
+            const int x = g.row0 + r, i = x / a.s.g;
+            load4<T>(static_cast<const T*>(a.Q) + (int64_t)(first + i) * a.q_t +
+                         (int64_t)(g.h * a.s.g + x - i * a.s.g) * a.q_h + c,
+                     a.wide, v);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] *= a.scale;
+        *reinterpret_cast<float4*>(Qs + r * QS + c) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+    float acc[RT][CH][CW], m[RT], l[RT];
+    int end[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int x = ty * RT + r;
+        end[r] = x >= g.rows ? 0 : (a.s.causal ? g.L - g.n + (g.row0 + x) / a.s.g + 1 : g.L);
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int k = 0; k < CW; ++k) acc[r][c][k] = 0.f;
+    }
+    for (int kt = g.t0; kt < g.t1; ++kt) {
+        const int k0 = kt * kN;
+        __syncthreads();
+        load_rows<E, D>(a, g, a.K, a.k_p, a.k_h, a.k_r, k0, KVs);
+        __syncthreads();
+        float s[RT][4];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[r][k] = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D; c += 4) {
+            float4 kv[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) kv[k] = *reinterpret_cast<const float4*>(KVs + (tx + 16 * k) * QS + c);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const float4 q = *reinterpret_cast<const float4*>(Qs + (ty * RT + r) * QS + c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    s[r][k] = fmaf(q.x, kv[k].x, s[r][k]);
+                    s[r][k] = fmaf(q.y, kv[k].y, s[r][k]);
+                    s[r][k] = fmaf(q.z, kv[k].z, s[r][k]);
+                    s[r][k] = fmaf(q.w, kv[k].w, s[r][k]);
+                }
+            }
+        }
+        __syncthreads();  // K has been read: V takes its place
+        load_rows<E, D>(a, g, a.V, a.v_p, a.v_h, a.v_r, k0, KVs);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            float best = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k0 + tx + 16 * k >= end[r]) s[r][k] = -INFINITY;
+                best = fmaxf(best, s[r][k]);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+            const float mn = fmaxf(m[r], best), base = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2f(m[r] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float p = exp2f(s[r][k] - base);
+                Ps[(ty * RT + r) * PS + tx + 16 * k] = p;
+                sum += p;
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l[r] = l[r] * f + sum;
+            m[r] = mn;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int k = 0; k < CW; ++k) acc[r][c][k] *= f;
+        }
+        __syncthreads();
+#pragma unroll 2
+        for (int j = 0; j < kN; j += 4) {
+            float4 p[RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) p[r] = *reinterpret_cast<const float4*>(Ps + (ty * RT + r) * PS + j);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    float v[CW];
+#pragma unroll
+                    for (int k = 0; k < CW; ++k) v[k] = KVs[(j + jj) * QS + c * 64 + tx * CW + k];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const float pr = jj == 0 ? p[r].x : jj == 1 ? p[r].y : jj == 2 ? p[r].z : p[r].w;
+#pragma unroll
+                        for (int k = 0; k < CW; ++k) acc[r][c][k] = fmaf(pr, v[k], acc[r][c][k]);
+                    }
+                }
+            }
+        }
+    }
+    const bool whole = g.t0 == 0 && g.t1 == g.nt;
+    const int64_t piece = ((int64_t)blockIdx.x * 2 + (g.t0 > 0 ? 0 : 1)) * kM;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int x = ty * RT + r;
+        if (x >= g.rows) continue;
+        if (whole) {
+            const int i = (g.row0 + x) / a.s.g, hq = g.h * a.s.g + g.row0 + x - i * a.s.g;
+            const float rcp = l[r] > 0.f || l[r] != l[r] ? 1.f / l[r] : 0.f;
+            T* o = static_cast<T*>(a.O) + (int64_t)(first + i) * a.o_t + (int64_t)hq * a.o_h;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int k = 0; k < CW; ++k) put(o + c * 64 + tx * CW + k, acc[r][c][k] * rcp);
+            if (a.lse && tx == 0)
+                a.lse[(int64_t)(first + i) * (a.s.Hkv * a.s.g) + hq] =
+                    l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * 0.6931471805599453f;
+        } else {
+            float* o = a.p.part + (piece + x) * D;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int k = 0; k < CW; ++k) o[c * 64 + tx * CW + k] = acc[r][c][k];
+            if (tx == 0) a.p.ml[piece + x] = make_float2(m[r], l[r]);
+        }
+    }
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
+    extern __shared__ __align__(16) float simt_sm[];
+    float* Qs = simt_sm;
+    float* KVs = Qs + kM * (D + kPad);
+    float* Ps = KVs + kN * (D + kPad);
+    const int64_t total = a.p.prefix[a.s.B];
+    const int active = active_blocks(total, a.G), c = blockIdx.x;
+    int4 join = make_int4(0, 0, 0, -1);
+    if (c < active) {
+        Walk<kM, kN> w;
+        w.start(a.s, a.p, block_start(total, active, c), block_start(total, active, c + 1));
+        Seg g;
+        while (w.next(a.s, g)) {
+            if (g.rows <= 16) simt_segment<E, D, 1>(a, g, Qs, KVs, Ps);
+            else simt_segment<E, D, 4>(a, g, Qs, KVs, Ps);
+            if (g.t0 > 0 && g.t1 == g.nt) join = make_int4(g.b, g.h, g.t, block_of(total, active, g.unit_start));
+        }
+    }
+    if (threadIdx.x == 0) a.p.joins[c] = join;
+}
+
+template <int M, int N>
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(Shape s, Plan p) {
+    plan_block<M, N>(s, p, &g_paged_attend_status);
+}
+
+template <typename E, int D>
+Status run_simt(const PagedAttendRequest& q, cudaStream_t st) {
+    using T = typename E::T;
+    const int G = 2 * paged_sm_count();
+    Carve cv(q.ws, q.ws_bytes);
+    SimtArgs a{};
+    carve_plan(cv, &a.p, q.B, G, kM, D);
+    if (!cv.fits()) return Status::fail(4, "paged_attend: workspace too small");
+    a.s = Shape{q.table, q.table_stride, q.W, q.seq_lens, q.cu_new, q.T, q.pages, (int)q.B, q.Hkv, q.Hq / q.Hkv,
+                q.page_size, q.causal};
+    a.Q = q.Q; a.K = q.K; a.V = q.V;
+    a.q_t = q.q_t; a.q_h = q.q_h;
+    a.k_p = q.k_p; a.k_h = q.k_h; a.k_r = q.k_r;
+    a.v_p = q.v_p; a.v_h = q.v_h; a.v_r = q.v_r;
+    a.O = q.O; a.o_t = q.o_t; a.o_h = q.o_h;
+    a.lse = q.lse;
+    a.scale = q.beta * 1.4426950408889634f;
+    a.G = G;
+    const int64_t all = q.q_t | q.q_h | q.k_p | q.k_h | q.k_r | q.v_p | q.v_h | q.v_r;
+    const uintptr_t ptrs = reinterpret_cast<uintptr_t>(q.Q) | reinterpret_cast<uintptr_t>(q.K) | reinterpret_cast<uintptr_t>(q.V);
+    a.wide = all % 4 == 0 && ptrs % (4 * sizeof(T)) == 0;
+    paged_plan_kernel<kM, kN><<<1, kPlanThreads, 0, st>>>(a.s, a.p);
+    const size_t smem = sizeof(float) * ((size_t)(kM + kN) * (D + kPad) + (size_t)kM * (kN + kPad));
+    cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return Status::cuda(e, "paged_attend: shared memory attribute");
+    paged_simt_kernel<E, D><<<G, kThreads, smem, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return Status::cuda(e, "paged_attend launch");
+    return launch_paged_join(PagedJoin{a.s, a.p, q.O, q.o_t, q.o_h, q.lse, G}, q.dtype, D, kM, st);
+}
+
+}  // namespace
+
+size_t paged_attend_workspace_bytes(int64_t B, int d) {
+    const int sms = paged_sm_count();
+    Plan p;
+    Carve a(nullptr, 0), b(nullptr, 0);
+    const size_t simt = carve_plan(a, &p, B, 2 * sms, kM, d), tc = carve_plan(b, &p, B, sms, kPagedTcRows, d);
+    return std::max(simt, tc) + 256;
+}
+
+Status launch_paged_attend(const PagedAttendRequest& q, cudaStream_t st) {
+    const bool bf = q.dtype == 1;
+    switch (q.d) {
+        case 32: return bf ? run_simt<BF16, 32>(q, st) : run_simt<F32, 32>(q, st);
+        case 64: return bf ? run_simt<BF16, 64>(q, st) : run_simt<F32, 64>(q, st);
+        case 128: return bf ? run_simt<BF16, 128>(q, st) : run_simt<F32, 128>(q, st);
+    }
+    return Status::fail(2, "paged_attend: unsupported head dim");
+}
+
+int read_paged_attend_status(bool clear) {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_paged_attend_status, sizeof(int)) != cudaSuccess) return -1;
+    if (clear && v) {
+        const int z = 0;
+        cudaMemcpyToSymbol(g_paged_attend_status, &z, sizeof(int));
+    }
+    return v;
+}
+
+}  // namespace wildcat
