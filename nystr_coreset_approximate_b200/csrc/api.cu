@@ -345,7 +345,7 @@ Status stage_host_inputs(HostPipe* hp, cudaStream_t s, void* Kd, void* Vd, void*
 namespace wildcat {
 int read_device_status(bool clear) {
     const int parts[] = {read_attend_status(clear), read_weights_status(clear), read_select_gs_status(clear),
-                         read_paged_status(clear), read_paged_attend_status(clear)};
+                         read_paged_status(clear), read_paged_attend_status(clear), read_paged_attend_tc_status(clear)};
     for (const int v : parts)
         if (v < 0) return -1;
     int worst = 0;  // an expired wait (5) before a bad slot, page id or length (1)

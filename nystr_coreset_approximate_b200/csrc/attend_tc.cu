@@ -67,8 +67,7 @@ namespace wildcat {
 
 __device__ int g_device_status = 0;  // WILDCAT_ERR_TIMEOUT when a bounded wait expired
 
-bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, int elem_bytes, const void* base, uint64_t d0,
-                  uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1) {
+static PFN_cuTensorMapEncodeTiled_v12000 tmap_encode() {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -80,6 +79,12 @@ bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, int elem_bytes, co
         else
             cudaGetLastError();
     });
+    return encode;
+}
+
+bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, int elem_bytes, const void* base, uint64_t d0,
+                  uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encode();
     if (!encode || (reinterpret_cast<uintptr_t>(base) & 15u) || (s1 & 15u) || (s2 & 15u) ||
         b0 * (uint32_t)elem_bytes != 128u)
         return false;
@@ -88,6 +93,26 @@ bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, int elem_bytes, co
     const cuuint32_t box[3] = {b0, b1, 1};
     const cuuint32_t es[3] = {1, 1, 1};
     return encode(map, type, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_tmap_4d(CUtensorMap* map, CUtensorMapDataType type, int elem_bytes, const void* base,
+                  const uint64_t (&dims)[4], const uint64_t (&strides)[3], const uint32_t (&box)[4]) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encode();
+    if (!encode || (reinterpret_cast<uintptr_t>(base) & 15u) || box[0] * (uint32_t)elem_bytes != 128u) return false;
+    cuuint64_t d[4], s[3];
+    cuuint32_t b[4], es[4];
+    for (int k = 0; k < 4; ++k) {
+        d[k] = dims[k];
+        b[k] = box[k];
+        es[k] = 1;
+    }
+    for (int k = 0; k < 3; ++k) {
+        s[k] = dims[k + 1] == 1 ? dims[0] * (uint64_t)elem_bytes : strides[k];
+        if (s[k] & 15u) return false;
+    }
+    return encode(map, type, 4, const_cast<void*>(base), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -42,22 +42,22 @@ struct Shape {
     const int32_t* seq_lens;
     const int32_t* cu_new;
     int64_t T, pages;
-    int B, Hkv, g, page_size;
+    int B, Hkv, g, page_size, M;
     bool causal;
 
     __device__ __forceinline__ int first_row(int b) const {
         return (int)min(max((int64_t)cu_new[b], (int64_t)0), T);
     }
     __device__ __forceinline__ int new_tokens(int b) const { return max(first_row(b + 1) - first_row(b), 0); }
-    // a length past the table's pages is cut to them (and reported by the plan)
-    __device__ __forceinline__ int length(int b) const {
-        return (int)min((int64_t)max(seq_lens[b], 0), min(W * page_size, (int64_t)0x7fffffff));
-    }
+    // a length past the table's pages is cut to them (and reported by the plan); so is one
+    // whose last key tile would end past 2^31
+    __device__ __forceinline__ int64_t most() const { return min(W * page_size, (int64_t)0x7fffff00); }
+    __device__ __forceinline__ int length(int b) const { return (int)min((int64_t)max(seq_lens[b], 0), most()); }
 };
 
 // Key tiles of row tile t (at least one: rows that see nothing are written too).
-template <int M, int N>
-__device__ __forceinline__ int unit_tiles(int n, int L, int g, bool causal, int64_t t) {
+template <int N>
+__device__ __forceinline__ int unit_tiles(int M, int n, int L, int g, bool causal, int64_t t) {
     int end = L;
     if (causal) {
         const int64_t last = min((t * M + M - 1) / g, (int64_t)n - 1);  // the tile's last token
@@ -73,7 +73,7 @@ struct Seg {
 };
 
 // The segments of one block, in order.
-template <int M, int N>
+template <int N>
 struct Walk {
     int64_t pos, hi;
     int b, h, n, L, tiles, off;
@@ -97,18 +97,18 @@ struct Walk {
         h = (int)(rem / ph);
         rem -= (int64_t)h * ph;
         t = 0;
-        int nt = unit_tiles<M, N>(n, L, s.g, s.causal, 0);
+        int nt = unit_tiles<N>(s.M, n, L, s.g, s.causal, 0);
         while (rem >= nt) {
             rem -= nt;
             ++t;
-            nt = unit_tiles<M, N>(n, L, s.g, s.causal, t);
+            nt = unit_tiles<N>(s.M, n, L, s.g, s.causal, t);
         }
         off = (int)rem;
     }
     __device__ __forceinline__ void load(const Shape& s) {
         n = s.new_tokens(b);
         L = s.length(b);
-        tiles = (int)(((int64_t)n * s.g + M - 1) / M);
+        tiles = (int)(((int64_t)n * s.g + s.M - 1) / s.M);
     }
     __device__ bool next(const Shape& s, Seg& o) {
         if (pos >= hi) return false;
@@ -117,9 +117,9 @@ struct Walk {
         o.n = n;
         o.L = L;
         o.t = (int)t;
-        o.row0 = (int)(t * M);
-        o.rows = (int)min((int64_t)M, (int64_t)n * s.g - t * M);
-        o.nt = unit_tiles<M, N>(n, L, s.g, s.causal, t);
+        o.row0 = (int)(t * s.M);
+        o.rows = (int)min((int64_t)s.M, (int64_t)n * s.g - t * s.M);
+        o.nt = unit_tiles<N>(s.M, n, L, s.g, s.causal, t);
         o.t0 = off;
         o.unit_start = pos - off;
         o.t1 = (int)min((int64_t)o.nt, off + (hi - pos));
@@ -153,7 +153,7 @@ __device__ __forceinline__ int block_of(int64_t total, int active, int64_t x) {
 }
 
 // prefix and per_head from the lengths: one block.
-template <int M, int N>
+template <int N>
 __device__ void plan_block(const Shape& s, const Plan& p, int* status) {
     __shared__ int64_t warp_sums[32];
     __shared__ int64_t carry;
@@ -165,14 +165,14 @@ __device__ void plan_block(const Shape& s, const Plan& p, int* status) {
         int64_t tiles = 0;
         if (b < s.B) {
             const int n = s.new_tokens(b), L = s.length(b);
-            if ((int64_t)s.seq_lens[b] > s.W * s.page_size || s.seq_lens[b] < 0 || s.cu_new[b] < 0 ||
+            if ((int64_t)s.seq_lens[b] > s.most() || s.seq_lens[b] < 0 || s.cu_new[b] < 0 ||
                 s.cu_new[b + 1] < s.cu_new[b] || s.cu_new[b + 1] > s.T)
-                atomicExch(status, 1);
-            const int64_t row_tiles = ((int64_t)n * s.g + M - 1) / M;
+                atomicMax(status, 1);
+            const int64_t row_tiles = ((int64_t)n * s.g + s.M - 1) / s.M;
             if (s.causal)
-                for (int64_t t = 0; t < row_tiles; ++t) tiles += unit_tiles<M, N>(n, L, s.g, true, t);
+                for (int64_t t = 0; t < row_tiles; ++t) tiles += unit_tiles<N>(s.M, n, L, s.g, true, t);
             else if (row_tiles > 0)
-                tiles = row_tiles * unit_tiles<M, N>(n, L, s.g, false, 0);
+                tiles = row_tiles * unit_tiles<N>(s.M, n, L, s.g, false, 0);
             p.per_head[b] = tiles;
         }
         int64_t x = tiles * s.Hkv;
@@ -196,7 +196,7 @@ __device__ void plan_block(const Shape& s, const Plan& p, int* status) {
 
 }  // namespace paged
 
-constexpr int kPagedTcRows = 256;  // rows of a unit of the tensor-core kernel
+constexpr int kPagedTcRows = 256;  // rows of a unit of the tensor-core kernel, at most
 
 struct PagedJoin {
     paged::Shape s;
@@ -206,6 +206,7 @@ struct PagedJoin {
     float* lse;
     int G;
 };
+// M: rows of a piece
 Status launch_paged_join(const PagedJoin& a, int dtype, int d, int M, cudaStream_t stream);
 
 }  // namespace wildcat

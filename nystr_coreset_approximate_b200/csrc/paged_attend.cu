@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     const int active = active_blocks(total, a.G), c = blockIdx.x;
     int4 join = make_int4(0, 0, 0, -1);
     if (c < active) {
-        Walk<kM, kN> w;
+        Walk<kN> w;
         w.start(a.s, a.p, block_start(total, active, c), block_start(total, active, c + 1));
         Seg g;
         while (w.next(a.s, g)) {
@@ -275,9 +275,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     if (threadIdx.x == 0) a.p.joins[c] = join;
 }
 
-template <int M, int N>
+template <int N>
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(Shape s, Plan p) {
-    plan_block<M, N>(s, p, &g_paged_attend_status);
+    plan_block<N>(s, p, &g_paged_attend_status);
 }
 
 template <typename E, int D>
@@ -289,7 +289,7 @@ Status run_simt(const PagedAttendRequest& q, cudaStream_t st) {
     carve_plan(cv, &a.p, q.B, G, kM, D);
     if (!cv.fits()) return Status::fail(4, "paged_attend: workspace too small");
     a.s = Shape{q.table, q.table_stride, q.W, q.seq_lens, q.cu_new, q.T, q.pages, (int)q.B, q.Hkv, q.Hq / q.Hkv,
-                q.page_size, q.causal};
+                q.page_size, kM, q.causal};
     a.Q = q.Q; a.K = q.K; a.V = q.V;
     a.q_t = q.q_t; a.q_h = q.q_h;
     a.k_p = q.k_p; a.k_h = q.k_h; a.k_r = q.k_r;
@@ -301,7 +301,7 @@ Status run_simt(const PagedAttendRequest& q, cudaStream_t st) {
     const int64_t all = q.q_t | q.q_h | q.k_p | q.k_h | q.k_r | q.v_p | q.v_h | q.v_r;
     const uintptr_t ptrs = reinterpret_cast<uintptr_t>(q.Q) | reinterpret_cast<uintptr_t>(q.K) | reinterpret_cast<uintptr_t>(q.V);
     a.wide = all % 4 == 0 && ptrs % (4 * sizeof(T)) == 0;
-    paged_plan_kernel<kM, kN><<<1, kPlanThreads, 0, st>>>(a.s, a.p);
+    paged_plan_kernel<kN><<<1, kPlanThreads, 0, st>>>(a.s, a.p);
     const size_t smem = sizeof(float) * ((size_t)(kM + kN) * (D + kPad) + (size_t)kM * (kN + kPad));
     cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return Status::cuda(e, "paged_attend: shared memory attribute");
@@ -323,6 +323,7 @@ size_t paged_attend_workspace_bytes(int64_t B, int d) {
 
 Status launch_paged_attend(const PagedAttendRequest& q, cudaStream_t st) {
     const bool bf = q.dtype == 1;
+    if (paged_attend_tc_supported(q)) return launch_paged_attend_tc(q, st);
     switch (q.d) {
         case 32: return bf ? run_simt<BF16, 32>(q, st) : run_simt<F32, 32>(q, st);
         case 64: return bf ? run_simt<BF16, 64>(q, st) : run_simt<F32, 64>(q, st);

@@ -23,13 +23,15 @@ constexpr int kJoinThreads = 256, kJoinSplit = 4;
 template <typename E, int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedJoin a, int M) {
     using T = typename E::T;
+    // the attention's grid has finished, and its writes are visible
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x;
     const int4 j = a.p.joins[c];
     if (j.w < 0) return;
     const int c0 = j.w, pieces = c - c0 + 1;
     const int n = a.s.new_tokens(j.x), first = a.s.first_row(j.x);
-    const int64_t row0 = (int64_t)j.z * M;
-    const int rows = (int)min((int64_t)M, (int64_t)n * a.s.g - row0);
+    const int64_t row0 = (int64_t)j.z * a.s.M;
+    const int rows = (int)min((int64_t)a.s.M, (int64_t)n * a.s.g - row0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int W = D / 32;
     for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < rows; r += kJoinSplit * (kJoinThreads / 32)) {
@@ -79,8 +81,17 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedJoin a, i
 
 template <typename E, int D>
 Status run_join(const PagedJoin& a, int M, cudaStream_t st) {
-    paged_join_kernel<E, D><<<dim3((unsigned)a.G, kJoinSplit), kJoinThreads, 0, st>>>(a, M);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.G, kJoinSplit);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, paged_join_kernel<E, D>, a, M);
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return Status::cuda(e, "paged_attend: join launch");
     return Status::ok();
 }

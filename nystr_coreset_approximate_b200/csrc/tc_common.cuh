@@ -157,6 +157,13 @@ __device__ __forceinline__ void tma_load_3d(unsigned dst, const void* tmap, int 
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(mbar))
         : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(unsigned dst, const void* tmap, int x, int y, int z, int w, void* mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(mbar))
+        : "memory");
+}
 // 3-D tiled TMA store from shared memory (bulk-group completion).
 __device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int z, unsigned src) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
@@ -232,6 +239,14 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
     unsigned long long B = *reinterpret_cast<unsigned long long*>(&b);
     unsigned long long C = *reinterpret_cast<unsigned long long*>(&c);
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(C) : "l"(A), "l"(B));
+    return *reinterpret_cast<float2*>(&C);
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    unsigned long long A = *reinterpret_cast<unsigned long long*>(&a);
+    unsigned long long B = *reinterpret_cast<unsigned long long*>(&b);
+    unsigned long long C;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(C) : "l"(A), "l"(B));
     return *reinterpret_cast<float2*>(&C);
 }
 

@@ -18,4 +18,9 @@ namespace wildcat {
 bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, int elem_bytes, const void* base, uint64_t d0,
                   uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1);
 
+// The same for a 4-D tensor [d3][d2][d1][d0] with strides s1, s2, s3 and a box of
+// (b0, b1, b2, b3) elements.  The stride of a dimension of extent 1 does not matter.
+bool make_tmap_4d(CUtensorMap* map, CUtensorMapDataType type, int elem_bytes, const void* base,
+                  const uint64_t (&dims)[4], const uint64_t (&strides)[3], const uint32_t (&box)[4]);
+
 }  // namespace wildcat
