@@ -16,16 +16,22 @@
 // with a running maximum and sum of its own for each (HBM bounds it), which the
 // epilogue adds up.  The issue order is S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...,
 // across units: while one slot's scores are exponentiated the other's products
-// run.  K and V tiles pass through one ring of stages in the order of first use.
-// Warp roles:
-//   warp 0      producer: block-table lookups (one lane per page) and TMA
-//   warp 1      tensor cores (one thread issues)
-//   warp 2      zeroes the rows of V at or past the request's length in its last
-//               key tile: what the page holds there may be NaN, and 0 NaN is NaN
+// run, and S(k + 2) may overwrite P(k), which PV(k) has read (products run in
+// issue order).  Warp roles:
+//   warp 0      copies K tiles: page lookups (one lane per page) and TMA
+//   warp 1      tensor cores.  All of its code is on the path between two
+//               products, so it keeps only counters
+//   warp 2      cuts the block's share into segments (one unit's key tiles) and
+//               hands them to the other roles through a ring; follows the V
+//               tiles and zeroes their rows at or past the request's length:
+//               what the page holds there may be NaN, and 0 NaN is NaN
+//   warp 3      copies Q and V tiles
 //   warps 4-7   softmax of slot 0, warps 8-11 of slot 1, one row per thread.  The
-//               maximum is raised only when a row's grows by more than 2^8 (sums
-//               in float32 hold that; a bf16 P is as exact at 2^8 as at 1), so
-//               the accumulator is hardly ever rescaled
+//               exponentials are formed with the maximum of the tiles before;
+//               only when a row's grows by more than 2^8 is it raised, O rescaled
+//               and the tile done again (sums in float32 hold 2^8, and a bf16 P is
+//               as exact there as at 1), so that the tile's maximum is not on the
+//               path from S to P
 //   warps 12-15 epilogue: O / l as bf16, or a partial sum of a unit that is cut
 // P is rounded to bf16 for the product (the operand type of V); the sum l is
 // float32 of the unrounded P.
@@ -59,13 +65,21 @@ constexpr int kPlanThreads = 512;
 constexpr int kRegsLow = 96, kRegsSoftmax = 168, kRegsEpilogue = 80;
 static_assert(kRegsLow + 2 * kRegsSoftmax + kRegsEpilogue == 512, "register split");
 constexpr unsigned long long kDrainNs = 100000000ull;
-constexpr float kRaise = 8.0f;  // the maximum is raised when a row's grows by more (powers of two)
+constexpr int kItems = 8;  // segments in the ring
+constexpr int kLead = 5;   // segments that warp 2 hands out ahead of its own
+constexpr int kAhead = 3;  // key tiles between the first touch of their page ids and their use
 
-template <int NS>
+// One segment: key tiles [t0, t1) of a unit; t1 == t0 ends the ring.
+struct Item {
+    int b, h, t, n, L, row0, rows, t0, t1, nt, first, join;
+};
+
+template <int NK, int NV>
 struct Bars {
     uint64_t q_full[2], q_free[2];
-    uint64_t full[NS], fixed[NS], empty[NS];
-    uint64_t s_full[2], p_full[2], pv_done[2], o_full[2], o_free[2], den_full[2];
+    uint64_t k_full[NK], k_empty[NK], v_full[NV], v_fixed[NV], v_empty[NV];
+    uint64_t s_full[2], p_full[2], o_full[2], o_free[2], den_full[2];
+    uint64_t item_full[kItems], item_empty[kItems];
     uint64_t drain;
     unsigned tmem_base;
     int abort;
@@ -74,15 +88,18 @@ struct Bars {
 template <int D>
 struct Cfg {
     static constexpr int KB = D / 64;                   // 128-byte blocks of a row
-    static constexpr int NS = D == 128 ? 5 : 12;        // stages of the ring of K and V tiles
+    static constexpr int NK = D == 128 ? 3 : 6;         // stages of K tiles: two operations more are on their way
+    static constexpr int NV = D == 128 ? 2 : 6;         // stages of V tiles
     static constexpr uint32_t q_bytes = kRows * D * 2;  // one row tile
     static constexpr uint32_t t_bytes = kKeys * D * 2;  // one tile of K or V
     static constexpr uint32_t blk = kKeys * 128;        // one 128-byte block of a tile
     static constexpr uint32_t off_q = 0;
-    static constexpr uint32_t off_t = off_q + 2 * q_bytes;
-    static constexpr uint32_t off_ml = off_t + NS * t_bytes;  // (m, l) of each slot's rows
-    static constexpr uint32_t off_bar = off_ml + 2 * kRows * 8;
-    static constexpr uint32_t total = off_bar + (uint32_t)sizeof(Bars<NS>);
+    static constexpr uint32_t off_k = off_q + 2 * q_bytes;
+    static constexpr uint32_t off_v = off_k + NK * t_bytes;
+    static constexpr uint32_t off_ml = off_v + NV * t_bytes;  // (m, l) of each slot's rows
+    static constexpr uint32_t off_items = off_ml + 2 * kRows * 8;
+    static constexpr uint32_t off_bar = off_items + kItems * (uint32_t)sizeof(Item);
+    static constexpr uint32_t total = off_bar + (uint32_t)sizeof(Bars<NK, NV>);
     static constexpr unsigned tmem_cols = 512;
     static constexpr unsigned col_O = 0;      // O of slot t at t * D
     static constexpr unsigned col_S = 2 * D;  // S of slot t at 2 D + 128 t
@@ -100,284 +117,366 @@ struct TcArgs {
     int box;      // rows of a page in one copy: min(page_size, 128)
 };
 
-// The operations of one block, in order.
-struct Ops {
-    Walk<kKeys> w;
-    Seg g;
-    int i, n;      // operation of the segment, and how many it has
-    unsigned k0;   // number of its first operation
-    unsigned q0;   // row tiles loaded before it
-    bool two;      // two row tiles
-    bool valid;
-
-    __device__ __forceinline__ void load(int R) {
-        two = g.rows > R;
-        n = (g.t1 - g.t0) << (two ? 1 : 0);
-        i = 0;
-    }
-    __device__ __forceinline__ void start(const TcArgs& a, int64_t lo, int64_t hi) {
-        w.start(a.s, a.p, lo, hi);
-        k0 = q0 = 0;
-        valid = w.next(a.s, g);
-        if (valid) load(a.R);
-    }
-    __device__ __forceinline__ void next_seg(const TcArgs& a) {
-        k0 += n;
-        q0 += two ? 2 : 1;
-        valid = w.next(a.s, g);
-        if (valid) load(a.R);
-    }
-    __device__ __forceinline__ void next(const TcArgs& a) {
-        if (++i == n) next_seg(a);
-    }
-    __device__ __forceinline__ int slot() const { return (int)((k0 + i) & 1u); }
-    __device__ __forceinline__ int tile() const { return two ? i & 1 : 0; }  // row tile
-    __device__ __forceinline__ int key_tile() const { return g.t0 + (two ? i >> 1 : i); }
-    __device__ __forceinline__ bool first() const { return i < 2; }  // of its slot in the segment
-    __device__ __forceinline__ bool last() const { return i >= n - 2; }
-    __device__ __forceinline__ bool opens() const { return !two || !(i & 1); }  // first use of the key tile
-    __device__ __forceinline__ bool closes() const { return !two || (i & 1); }  // last use
-    __device__ __forceinline__ int q_buf() const { return (int)((q0 + tile()) & 1u); }
-    __device__ __forceinline__ bool q_opens() const { return i < (two ? 2 : 1); }
-    __device__ __forceinline__ bool q_closes() const { return i >= n - (two ? 2 : 1); }
-    // rows of V past the length in this key tile
-    __device__ __forceinline__ bool tail() const { return (key_tile() + 1) * kKeys > g.L; }
-};
-
 template <int D>
 struct Ctx {
     unsigned char* sm;
     unsigned sbase, tmem;
-    Bars<Cfg<D>::NS>* bars;
+    Bars<Cfg<D>::NK, Cfg<D>::NV>* bars;
     volatile int* abort_flag;
-    int64_t lo, hi;
     __device__ void give_up() const {
         *abort_flag = 1;
         atomicMax(&g_paged_tc_status, 5);
     }
+    // a wait of a whole warp
+    __device__ __forceinline__ bool wait(uint64_t* b, unsigned parity) const {
+        return __all_sync(0xffffffffu, mbar_wait_suspend(b, parity & 1u, abort_flag));
+    }
+    __device__ __forceinline__ Item* item(unsigned s) const {
+        return reinterpret_cast<Item*>(sm + Cfg<D>::off_items) + s % kItems;
+    }
+    // segment s once it is in the ring
+    __device__ __forceinline__ bool item_wait(unsigned s) const { return wait(&bars->item_full[s % kItems], s / kItems); }
+    __device__ __forceinline__ bool item_there(unsigned s) const {
+        return __all_sync(0xffffffffu, mbar_try(smem_u32(&bars->item_full[s % kItems]), (s / kItems) & 1u));
+    }
+    // this warp has read segment s
+    __device__ __forceinline__ void item_done(unsigned s, int lane) const {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->item_empty[s % kItems]);
+    }
+};
+constexpr int kItemReaders = 3 + 8 + 4;  // warps 0, 1, 3, the softmax groups, the epilogue
+
+// A place in a ring of N stages and the parity of its use.
+template <int N>
+struct Ring {
+    int s = 0;
+    unsigned ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == N) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
 };
 
-// Warp 0.  All lanes walk alike; lane p looks up and copies page p of a tile.
+// The page ids of a segment's key tiles: lane p has page p of a tile.
 template <int D>
-__device__ __forceinline__ void role_producer(const Ctx<D>& x, const TcArgs& a, const CUtensorMap* tmQ,
-                                              const CUtensorMap* tmK, const CUtensorMap* tmV, int lane) {
-    using C = Cfg<D>;
-    constexpr int NS = C::NS;
-    auto* bars = x.bars;
-    if (lane == 0) {
-        prefetch_tmap(tmQ);
-        prefetch_tmap(tmK);
-        prefetch_tmap(tmV);
+struct Pages {
+    const int32_t* row;  // the request's row of the table
+    int L, t1;
+
+    __device__ __forceinline__ void of(const TcArgs& a, const Item& g) {
+        row = a.s.table + (int64_t)g.b * a.s.table_stride;
+        L = g.L;
+        t1 = g.t1;
     }
-    unsigned n = 0, qn = 0;  // tiles and row tiles issued
-    bool ok = true;
-    auto put_tile = [&](const Ops& o, const CUtensorMap* tm) {
-        const int s = (int)(n % NS);
-        if (n >= NS) {
-            ok = __all_sync(0xffffffffu, mbar_wait_suspend(&bars->empty[s], (n / NS - 1) & 1u, x.abort_flag));
-            if (!ok) return;
+    // the copy of a page past the pool fills zeros
+    __device__ __forceinline__ int id(const TcArgs& a, int kt, int lane) const {
+        const int j = kt * kKeys + lane * a.box;
+        int page = (int)a.s.pages;
+        if (lane * a.box < kKeys && j < L) {
+            const int v = __ldg(row + (unsigned)j / (unsigned)a.s.page_size);
+            if (v >= 0 && v < a.s.pages) page = v;
+            else atomicMax(&g_paged_tc_status, 1);
         }
-        if (lane == 0) mbar_expect_tx(&bars->full[s], C::t_bytes);
-        __syncwarp();
-        const int boxes = kKeys / a.box;
-        if (lane < boxes) {
-            const int j = o.key_tile() * kKeys + lane * a.box, p = j / a.s.page_size;
-            int id = (int)a.s.pages;  // past the pool: the copy fills zeros
-            if (j < o.g.L) {
-                const int v = a.s.table[(int64_t)o.g.b * a.s.table_stride + p];
-                if (v >= 0 && v < a.s.pages) id = v;
-                else atomicMax(&g_paged_tc_status, 1);
-            }
-            const unsigned dst = x.sbase + C::off_t + (unsigned)s * C::t_bytes + (unsigned)(lane * a.box) * 128u;
+        return page;
+    }
+    // bring the ids of a later tile into L1: a lookup from L2 or HBM takes as long as a tile's copy
+    __device__ __forceinline__ void touch(const TcArgs& a, int kt, int lane) const {
+        const int j = kt * kKeys + lane * a.box;
+        if (kt < t1 && lane * a.box < kKeys && j < L) {
+            int dummy;
+            asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(dummy) : "l"(row + (unsigned)j / (unsigned)a.s.page_size));
+        }
+    }
+};
+
+// One tile of K or V, page by page, by one lane.
+template <int D>
+__device__ __forceinline__ void copy_tile(const TcArgs& a, const CUtensorMap* tm, unsigned dst, int kt, int h, int id,
+                                          uint64_t* full) {
+    using C = Cfg<D>;
+    const int boxes = kKeys / a.box;
+    const int row = boxes > 1 ? 0 : (int)((unsigned)(kt * kKeys) % (unsigned)a.s.page_size);
+    if (elect_one()) mbar_expect_tx(full, C::t_bytes);
+    __syncwarp();
+    for (int p0 = 0; p0 < boxes; p0 += 8) {
+        int page[8];
 #pragma unroll
-            for (int kb = 0; kb < C::KB; ++kb)
-                tma_load_4d(dst + kb * C::blk, tm, kb * 64, j - p * a.s.page_size, o.g.h, id, &bars->full[s]);
-        }
-        ++n;
-    };
-    auto put_k = [&](const Ops& o) {
-        if (o.q_opens()) {
-            const int qb = (int)(qn & 1u);
-            if (qn >= 2) {
-                ok = __all_sync(0xffffffffu, mbar_wait_suspend(&bars->q_free[qb], (qn / 2 - 1) & 1u, x.abort_flag));
-                if (!ok) return;
-            }
-            if (lane == 0) {
-                mbar_expect_tx(&bars->q_full[qb], (unsigned)a.R * 128u * C::KB);
-                const int token = a.s.first_row(o.g.b) + (o.g.row0 + o.tile() * a.R) / a.s.g;
+        for (int p = 0; p < 8; ++p) page[p] = __shfl_sync(0xffffffffu, id, p0 + p);
+        if (elect_one()) {
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                if (p0 + p >= boxes) break;
 #pragma unroll
                 for (int kb = 0; kb < C::KB; ++kb)
-                    tma_load_4d(x.sbase + C::off_q + (unsigned)qb * C::q_bytes + kb * (kRows * 128), tmQ, kb * 64, 0,
-                                o.g.h, token, &bars->q_full[qb]);
+                    tma_load_4d(dst + (unsigned)((p0 + p) * a.box) * 128u + kb * C::blk, tm, kb * 64, row, h, page[p], full);
             }
-            ++qn;
         }
-        if (o.opens()) put_tile(o, tmK);
-    };
-    Ops k, v;
-    k.start(a, x.lo, x.hi);
-    v = k;
-    for (int e = 0; e < 2 && k.valid && ok; ++e) {
-        put_k(k);
-        k.next(a);
+        __syncwarp();
     }
-    while (v.valid && ok) {
-        if (v.opens()) put_tile(v, tmV);
-        v.next(a);
+}
+
+// Warps 0 and 3: the K tiles (V false), or each segment's Q tiles and its V tiles.
+template <int D, bool V>
+__device__ __forceinline__ void role_copy(const Ctx<D>& x, const TcArgs& a, const CUtensorMap* tmQ, const CUtensorMap* tm,
+                                          int lane) {
+    using C = Cfg<D>;
+    constexpr int N = V ? C::NV : C::NK;
+    auto* bars = x.bars;
+    uint64_t* full = V ? bars->v_full : bars->k_full;
+    uint64_t* empty = V ? bars->v_empty : bars->k_empty;
+    const unsigned base = x.sbase + (V ? C::off_v : C::off_k);
+    if (lane == 0) {
+        prefetch_tmap(tm);
+        if (V) prefetch_tmap(tmQ);
+    }
+    Ring<N> r;
+    unsigned n = 0, qn = 0;  // tiles and row tiles issued
+    bool ok = true;
+    for (unsigned s = 0; ok; ++s) {
+        ok = x.item_wait(s);
         if (!ok) break;
-        if (k.valid) {
-            put_k(k);
-            k.next(a);
+        const Item g = *x.item(s);
+        x.item_done(s, lane);
+        if (g.t1 == g.t0) break;
+        Pages<D> pages;
+        pages.of(a, g);
+        for (int e = 0; e < kAhead; ++e) pages.touch(a, g.t0 + e, lane);
+        if (V) {
+            const int tiles = g.rows > a.R ? 2 : 1;
+            for (int e = 0; e < tiles && ok; ++e, ++qn) {
+                const unsigned qb = qn & 1u;
+                if (qn >= 2) ok = x.wait(&bars->q_free[qb], qn / 2 - 1);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_expect_tx(&bars->q_full[qb], (unsigned)a.R * 128u * C::KB);
+                    const int token = g.first + (g.row0 + e * a.R) / a.s.g;
+#pragma unroll
+                    for (int kb = 0; kb < C::KB; ++kb)
+                        tma_load_4d(x.sbase + C::off_q + qb * C::q_bytes + kb * (kRows * 128), tmQ, kb * 64, 0, g.h, token,
+                                    &bars->q_full[qb]);
+                }
+                __syncwarp();
+            }
+        }
+        for (int kt = g.t0; kt < g.t1 && ok; ++kt, r.next(), ++n) {
+            pages.touch(a, kt + kAhead, lane);
+            const int id = pages.id(a, kt, lane);
+            if (n >= N) ok = x.wait(&empty[r.s], r.ph ^ 1u);
+            if (!ok) break;
+            copy_tile<D>(a, tm, base + (unsigned)r.s * C::t_bytes, kt, g.h, id, &full[r.s]);
         }
     }
     if (!ok && lane == 0) x.give_up();
     __syncwarp();
     if (*x.abort_flag) {
         // copies still in flight land before the block's shared memory is released
-        if (qn > 0) mbar_wait(&bars->q_full[(qn - 1) & 1u], ((qn - 1) / 2) & 1u, kDrainNs);
-        if (qn > 1) mbar_wait(&bars->q_full[(qn - 2) & 1u], ((qn - 2) / 2) & 1u, kDrainNs);
-        for (unsigned c = n > NS ? n - NS : 0; c < n; ++c) mbar_wait(&bars->full[c % NS], (c / NS) & 1u, kDrainNs);
+        for (unsigned c = n > N ? n - N : 0; c < n; ++c) mbar_wait(&full[c % N], (c / N) & 1u, kDrainNs);
+        if (V)
+            for (unsigned c = qn > 2 ? qn - 2 : 0; c < qn; ++c) mbar_wait(&bars->q_full[c & 1u], (c / 2) & 1u, kDrainNs);
     }
 }
 
-// Warp 2: takes every tile of the ring in the producer's order, so that it is
-// never more than the ring's length away from the other roles, and zeroes the
-// rows of V past the length before it hands a tile on.
+// Warp 2.
 template <int D>
-__device__ __forceinline__ void role_fix(const Ctx<D>& x, const TcArgs& a, int lane) {
+__device__ __forceinline__ void role_plan(const Ctx<D>& x, const TcArgs& a, int lane, int64_t lo, int64_t hi, int64_t total,
+                                          int active) {
     using C = Cfg<D>;
-    constexpr int NS = C::NS;
-    unsigned n = 0;
-    bool ok = true;
-    auto take = [&](int keep) {  // rows of the tile that stay as they are
-        const int s = (int)(n % NS);
-        ok = __all_sync(0xffffffffu, mbar_wait_suspend(&x.bars->full[s], (n / NS) & 1u, x.abort_flag));
-        if (!ok) return;
-        if (keep < kKeys) {
-            unsigned char* tile = x.sm + C::off_t + (unsigned)s * C::t_bytes;
-            for (int e = lane; e < (kKeys - keep) * 8; e += 32)
-#pragma unroll
-                for (int kb = 0; kb < C::KB; ++kb)
-                    *reinterpret_cast<uint4*>(tile + kb * C::blk + keep * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-            fence_async_smem();
+    auto* bars = x.bars;
+    Walk<kKeys> w;
+    w.start(a.s, a.p, lo, hi);
+    Ring<C::NV> r;
+    unsigned pushed = 0;
+    bool more = true, ok = true;
+    for (unsigned s = 0; ok; ++s) {
+        while (more && pushed < s + kLead && ok) {
+            if (pushed >= kItems) ok = x.wait(&bars->item_empty[pushed % kItems], pushed / kItems - 1);
+            if (!ok) break;
+            Seg g;
+            more = w.next(a.s, g);
+            if (lane == 0) {
+                Item* it = x.item(pushed);
+                if (more) {
+                    const bool ends = g.t0 > 0 && g.t1 == g.nt;  // the last piece of a cut unit
+                    *it = Item{g.b, g.h, g.t, g.n, g.L, g.row0, g.rows, g.t0, g.t1, g.nt, a.s.first_row(g.b),
+                               ends ? block_of(total, active, g.unit_start) : -1};
+                } else {
+                    it->t0 = it->t1 = 0;
+                }
+                mbar_arrive(&bars->item_full[pushed % kItems]);
+            }
+            __syncwarp();
+            ++pushed;
         }
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&x.bars->fixed[s]);
-            mbar_arrive(&x.bars->empty[s]);
-        }
-        ++n;
-    };
-    Ops k, v;
-    k.start(a, x.lo, x.hi);
-    v = k;
-    for (int e = 0; e < 2 && k.valid && ok; ++e) {
-        if (k.opens()) take(kKeys);
-        k.next(a);
-    }
-    while (v.valid && ok) {
-        if (v.opens()) take(v.tail() ? max(v.g.L - v.key_tile() * kKeys, 0) : kKeys);
-        v.next(a);
         if (!ok) break;
-        if (k.valid) {
-            if (k.opens()) take(kKeys);
-            k.next(a);
+        const Item* it = x.item(s);
+        const int t0 = it->t0, t1 = it->t1, L = it->L;
+        __syncwarp();
+        if (t0 == t1) break;
+        for (int kt = t0; kt < t1; ++kt, r.next()) {
+            ok = x.wait(&bars->v_full[r.s], r.ph);
+            if (!ok) break;
+            if ((kt + 1) * kKeys > L) {
+                const int keep = max(L - kt * kKeys, 0);
+                unsigned char* tile = x.sm + C::off_v + (unsigned)r.s * C::t_bytes;
+                for (int e = lane; e < (kKeys - keep) * 8; e += 32)
+#pragma unroll
+                    for (int kb = 0; kb < C::KB; ++kb)
+                        *reinterpret_cast<uint4*>(tile + kb * C::blk + keep * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(&bars->v_fixed[r.s]);
         }
     }
     if (!ok && lane == 0) x.give_up();
 }
 
+// S_t = Q K^T and O_t (+)= P_t V, one thread.
 template <int D>
-__device__ __forceinline__ void gemm_s(const Ctx<D>& x, int qb, unsigned stage, int t) {  // S_t = Q K^T
-    using C = Cfg<D>;
-    const uint64_t da = umma_desc(x.sbase + C::off_q + (unsigned)qb * C::q_bytes);
-    const uint64_t db = umma_desc(x.sbase + C::off_t + stage * C::t_bytes);
-    const uint32_t hi = (uint32_t)(da >> 32), a_lo = (uint32_t)da, b_lo = (uint32_t)db;
+__device__ __forceinline__ void gemm_s(unsigned tmem_s, uint32_t q_lo, uint32_t k_lo, uint32_t hi) {
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t o = (uint32_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4);
-        mma_bf16_w(x.tmem + C::col_S + t * kKeys, a_lo + o, hi, b_lo + o, hi, idesc_bf16(128, kKeys), kk > 0);
+        mma_bf16_w(tmem_s, q_lo + o, hi, k_lo + o, hi, idesc_bf16(128, kKeys), kk > 0);
     }
 }
 template <int D>
-__device__ __forceinline__ void gemm_pv(const Ctx<D>& x, unsigned stage, int t, bool first) {  // O_t (+)= P_t V
-    using C = Cfg<D>;
-    const uint64_t db = umma_desc_mn(x.sbase + C::off_t + stage * C::t_bytes, C::blk);
-    const uint32_t hi = (uint32_t)(db >> 32), b_lo = (uint32_t)db;
+__device__ __forceinline__ void gemm_pv(unsigned tmem_o, unsigned tmem_p, uint32_t v_lo, uint32_t hi, bool first) {
 #pragma unroll
     for (int kk = 0; kk < kKeys / 16; ++kk)
-        mma_bf16_ts_w(x.tmem + C::col_O + t * D, x.tmem + C::col_S + t * kKeys + kk * 8, b_lo + (uint32_t)((kk * 2048) >> 4),
-                      hi, idesc_bf16_bmn(128, D), (!first || kk > 0) ? 1 : 0);
+        mma_bf16_ts_w(tmem_o, tmem_p + kk * 8, v_lo + (uint32_t)((kk * 2048) >> 4), hi, idesc_bf16_bmn(128, D),
+                      (!first || kk > 0) ? 1 : 0);
 }
 
-// Warp 1, one thread.
+// The operations of a segment as warp 1 sees them.
+struct OpCursor {
+    unsigned s;   // segment
+    int i, n;     // operation of n
+    bool two, valid;
+    __device__ __forceinline__ bool opens() const { return !two || !(i & 1); }  // first use of the key tile
+    __device__ __forceinline__ bool closes() const { return !two || (i & 1); }  // last use
+    __device__ __forceinline__ bool q_opens() const { return i < (two ? 2 : 1); }
+    __device__ __forceinline__ bool q_closes() const { return i >= n - (two ? 2 : 1); }
+    __device__ __forceinline__ bool first() const { return i < 2; }  // of its slot in the segment
+    __device__ __forceinline__ bool last() const { return i >= n - 2; }
+    template <int D>
+    __device__ __forceinline__ bool load(const Ctx<D>& x, int R) {
+        if (!x.item_wait(s)) return false;
+        const Item* it = x.item(s);
+        two = it->rows > R;
+        n = (it->t1 - it->t0) << (two ? 1 : 0);
+        i = 0;
+        valid = n > 0;
+        return true;
+    }
+};
+
+// Warp 1.  All lanes walk alike, one issues.
 template <int D>
-__device__ __forceinline__ void role_mma(const Ctx<D>& x, const TcArgs& a) {
+__device__ __forceinline__ void role_mma(const Ctx<D>& x, const TcArgs& a, int lane) {
     using C = Cfg<D>;
-    constexpr int NS = C::NS;
     auto* bars = x.bars;
-    unsigned n = 0;               // tiles taken from the ring
-    unsigned ks = 0, vs = 0;      // the ring's index of the current K and V tile
-    unsigned qn = 0;              // row tiles taken
-    unsigned pn[2] = {0, 0};      // operations of each slot
-    unsigned on[2] = {0, 0};      // segments of each slot
-    bool ok = true;
-    auto wait = [&](uint64_t* b, unsigned parity) { return mbar_wait_suspend(b, parity & 1u, x.abort_flag); };
-    auto scores = [&](const Ops& o) {
-        if (o.opens()) ks = n++;
-        if (!wait(&bars->full[ks % NS], ks / NS)) return false;
-        if (o.q_opens()) {
-            if (!wait(&bars->q_full[qn & 1u], qn / 2)) return false;
+    const uint64_t dk = umma_desc(x.sbase + C::off_k), dv = umma_desc_mn(x.sbase + C::off_v, C::blk);
+    const uint32_t q_lo = (uint32_t)umma_desc(x.sbase + C::off_q), k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
+    const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
+    Ring<C::NK> kr;  // the current K and V tile, and the next ones
+    Ring<C::NV> vr;
+    int ks = 0, vs = 0;
+    unsigned qn = 0;            // row tiles taken
+    unsigned q0 = 0;            // row tile of the S cursor's segment
+    unsigned kt = 0, vt = 0;    // slot of the next S and the next PV
+    unsigned pn[2] = {0, 0};    // operations of each slot
+    unsigned on[2] = {0, 0};    // accumulations of each slot
+    bool ok;
+    OpCursor k, v;
+    k.s = 0;
+    ok = k.load(x, a.R);
+    v = k;
+    auto ready = [&]() {  // K, and Q, of the next S have arrived
+        if (k.opens()) {
+            ks = kr.s;
+            if (!x.wait(&bars->k_full[kr.s], kr.ph)) return false;
+            kr.next();
+        }
+        if (k.q_opens()) {
+            if (!x.wait(&bars->q_full[qn & 1u], qn / 2)) return false;
             ++qn;
         }
-        tc_fence_after();
-        const int t = o.slot();
-        gemm_s<D>(x, o.q_buf(), ks % NS, t);
-        mma_commit(&bars->s_full[t]);
-        if (o.closes()) mma_commit(&bars->empty[ks % NS]);
-        if (o.q_closes()) mma_commit(&bars->q_free[o.q_buf()]);
         return true;
     };
-    Ops k, v;
-    k.start(a, x.lo, x.hi);
-    v = k;
-    for (int e = 0; e < 2 && k.valid && ok; ++e) {
-        ok = scores(k);
-        k.next(a);
-    }
-    while (v.valid && ok) {
-        const int t = v.slot();
-        if (v.opens()) vs = n++;
-        ok = wait(&bars->full[vs % NS], vs / NS);
-        if (ok && v.opens() && v.tail()) ok = wait(&bars->fixed[vs % NS], vs / NS);
-        ok = ok && wait(&bars->p_full[t], pn[t]++);
-        // the epilogue has taken the slot's previous O
-        if (ok && v.first()) {
-            if (on[t] > 0) ok = wait(&bars->o_free[t], on[t] - 1);
-            ++on[t];
+    auto scores = [&]() {  // one thread
+        const unsigned qb = (q0 + (k.two ? k.i & 1 : 0)) & 1u;
+        gemm_s<D>(x.tmem + C::col_S + kt * kKeys, q_lo + qb * (C::q_bytes >> 4), k_lo + (uint32_t)ks * (C::t_bytes >> 4), k_hi);
+        mma_commit(&bars->s_full[kt]);
+        if (k.closes()) mma_commit(&bars->k_empty[ks]);
+        if (k.q_closes()) mma_commit(&bars->q_free[qb]);
+    };
+    auto next_k = [&]() {
+        kt ^= 1u;
+        if (++k.i == k.n) {
+            q0 += k.two ? 2 : 1;
+            ++k.s;
+            ok = k.load(x, a.R);
         }
+    };
+    for (int e = 0; e < 2 && ok && k.valid; ++e) {
+        ok = ready();
         if (!ok) break;
         tc_fence_after();
-        gemm_pv<D>(x, vs % NS, t, v.first());
-        mma_commit(&bars->pv_done[t]);
-        if (v.last()) mma_commit(&bars->o_full[t]);
-        if (v.closes()) mma_commit(&bars->empty[vs % NS]);
-        v.next(a);
-        if (k.valid) {
-            // issued after the slot's product with V, which has read P out of these
-            // columns by the time this one writes them (products run in issue order)
-            ok = scores(k);
-            k.next(a);
+        if (elect_one()) scores();
+        __syncwarp();
+        next_k();
+    }
+    while (ok && v.valid) {
+        const unsigned t = vt;
+        if (v.opens()) {
+            vs = vr.s;
+            ok = x.wait(&bars->v_fixed[vr.s], vr.ph);
+            vr.next();
+        }
+        ok = ok && (!k.valid || ready());
+        if (ok && v.first()) {  // the epilogue has taken the slot's previous O
+            if (on[t] > 0) ok = x.wait(&bars->o_free[t], on[t] - 1);
+            ++on[t];
+        }
+        ok = ok && x.wait(&bars->p_full[t], pn[t]++);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+            gemm_pv<D>(x.tmem + C::col_O + t * D, x.tmem + C::col_S + t * kKeys, v_lo + (uint32_t)vs * (C::t_bytes >> 4), v_hi,
+                       v.first());
+            if (v.last()) mma_commit(&bars->o_full[t]);
+            if (v.closes()) mma_commit(&bars->v_empty[vs]);
+            // over the columns of P, which the product above has read by then
+            if (k.valid) scores();
+        }
+        __syncwarp();
+        if (k.valid) next_k();
+        vt ^= 1u;
+        if (ok && ++v.i == v.n) {
+            x.item_done(v.s, lane);
+            ++v.s;
+            ok = v.load(x, a.R);
         }
     }
-    if (!ok) x.give_up();
-    mma_commit(&bars->drain);
+    if (!ok && lane == 0) x.give_up();
+    if (elect_one()) mma_commit(&bars->drain);
+    __syncwarp();
     mbar_wait(&bars->drain, 0, kDrainNs);
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // Softmax of slot t: thread `row` owns row `row` of the slot's row tile.
 template <int D>
-__device__ __forceinline__ void role_softmax(const Ctx<D>& x, const TcArgs& a, int t, int quad, int lane) {
+__device__ __forceinline__ void role_softmax(const Ctx<D>& x, const TcArgs& a, unsigned t, int quad, int lane) {
     using C = Cfg<D>;
     auto* bars = x.bars;
     const int row = quad * 32 + lane;
@@ -386,111 +485,139 @@ __device__ __forceinline__ void role_softmax(const Ctx<D>& x, const TcArgs& a, i
     float2* ml = reinterpret_cast<float2*>(x.sm + C::off_ml) + t * kRows;
     const float2 a2 = make_float2(a.scale, a.scale);
     unsigned cs = 0, on = 0;  // operations and segments of this slot
-    float m = -INFINITY, l = 0.f;
-    int end = 0;
-    bool active = false, ok = true;
-    Ops o;
-    o.start(a, x.lo, x.hi);
-    for (; o.valid && ok; o.next(a)) {
-        if (o.slot() != t) continue;
-        if (o.first()) {
-            const int r = o.tile() * a.R + row;  // row of the unit
-            const int rows = min(o.g.rows - o.tile() * a.R, a.R);
-            active = quad * 32 < rows;
-            end = row < rows ? (a.s.causal ? o.g.L - o.g.n + (o.g.row0 + r) / a.s.g + 1 : o.g.L) : 0;
-            m = -INFINITY;
-            l = 0.f;
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait_suspend(&bars->s_full[t], cs & 1u, x.abort_flag));
+    unsigned k0 = 0;          // operations before the segment
+    bool ok = true;
+    for (unsigned s = 0; ok; ++s) {
+        ok = x.item_wait(s);
         if (!ok) break;
-        tc_fence_after();
-        if (active) {  // the same for all lanes of a warp
-            const int lim = end - o.key_tile() * kKeys;  // keys of this tile that the row sees
-            const bool edge = __any_sync(0xffffffffu, lim < kKeys);
-            uint32_t v[4][32];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) tmem_ld32_nowait(tS + 32 * j, v[j]);
-            tmem_wait_ld();
-            if (edge) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
+        int lim, step, ops, rows;
+        {
+            const Item g = *x.item(s);
+            x.item_done(s, lane);
+            if (g.t1 == g.t0) break;
+            const bool two = g.rows > a.R;
+            const int n = (g.t1 - g.t0) << (two ? 1 : 0), i0 = (int)((t ^ k0) & 1u);
+            k0 += n;
+            ops = (n - i0 + 1) >> 1;
+            const int tile = two ? i0 : 0, r = tile * a.R + row;
+            rows = min(g.rows - tile * a.R, a.R);
+            const int end = row < rows ? (a.s.causal ? g.L - g.n + (g.row0 + r) / a.s.g + 1 : g.L) : 0;
+            lim = end - (g.t0 + (two ? 0 : i0)) * kKeys;  // keys of the tile that the row sees
+            step = two ? kKeys : 2 * kKeys;
+        }
+        if (ops <= 0) continue;
+        const bool active = quad * 32 < rows;  // the same for all lanes of a warp
+        float m = -INFINITY, l = 0.f;
+        for (int c = 0; c < ops; ++c, lim -= step) {
+            ok = x.wait(&bars->s_full[t], cs);
+            if (!ok) break;
+            ++cs;
+            tc_fence_after();
+            if (active) {
+                const bool edge = __any_sync(0xffffffffu, lim < kKeys);
+                uint32_t v[4][32];
+                float2 sum[2], nb;
+                uint32_t top;
+                auto mask = [&](int j) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (32 * j + e >= lim) v[j][e] = 0xff800000u;
-            }
-            float best[4];
+                };
+                auto begin = [&]() {
+                    const float base = m == -INFINITY ? 0.f : m;
+                    nb = make_float2(-base, -base);
+                    sum[0] = sum[1] = make_float2(0.f, 0.f);
+                    top = 0u;
+                };
+                auto exps = [&](int j) {  // P of 32 keys
+                    uint32_t pk[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                best[j] = __uint_as_float(v[j][0]);
-#pragma unroll
-                for (int e = 1; e < 32; ++e) best[j] = fmaxf(best[j], __uint_as_float(v[j][e]));
-            }
-            const float mt = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * a.scale;
-            if (o.first()) {
-                m = mt;
-            } else {
-                const bool raise = mt > m + kRaise || (m == -INFINITY && mt > m);
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float f = raise ? ex2_approx(m - mt) : 1.f;
-                    if (raise) m = mt;
-                    l *= f;
-                    // the slot's previous product has been added to O
-                    ok = __all_sync(0xffffffffu, mbar_wait_suspend(&bars->pv_done[t], (cs - 1) & 1u, x.abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        float acc[16];
-                        uint32_t w[16];
-                        tmem_ld16(tO + c, acc);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(acc[e] * f);
-                        tmem_st16(tO + c, w);
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 y =
+                            ffma2(make_float2(__uint_as_float(v[j][2 * e]), __uint_as_float(v[j][2 * e + 1])), a2, nb);
+                        const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                        pk[e] = pack_bf16x2(p0, p1);
+                        sum[e & 1] = fadd2(sum[e & 1], make_float2(p0, p1));
+                        top = max_bf16x2(top, pk[e]);
                     }
-                    tmem_wait_st();
-                }
-            }
-            const float base = m == -INFINITY ? 0.f : m;
-            const float2 nb = make_float2(-base, -base);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    tmem_st16(tS + 16 * j, pk);
+                };
+                bool redo = c == 0;
+                if (c == 0) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t pk[16];
+                    for (int j = 0; j < 4; ++j) tmem_ld32_nowait(tS + 32 * j, v[j]);
+                    tmem_wait_ld();
+                    if (edge) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 y =
-                        ffma2(make_float2(__uint_as_float(v[j][2 * e]), __uint_as_float(v[j][2 * e + 1])), a2, nb);
-                    const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
-                    pk[e] = pack_bf16x2(p0, p1);
-                    sum[e & 1] = fadd2(sum[e & 1], make_float2(p0, p1));
+                        for (int j = 0; j < 4; ++j) mask(j);
+                    }
+                } else {
+                    begin();
+                    tmem_ld32_nowait(tS, v[0]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        tmem_wait_ld();
+                        if (j < 3) tmem_ld32_nowait(tS + 32 * (j + 1), v[j + 1]);
+                        if (edge) mask(j);
+                        exps(j);
+                    }
+                    // 2^8 in bf16 is 0x4380; P is not negative, so its bits order as numbers
+                    const bool high = (top & 0xffffu) > 0x4380u || (top >> 16) > 0x4380u;
+                    redo = __any_sync(0xffffffffu, high || (m == -INFINITY && lim > 0));
                 }
-                tmem_st16(tS + 16 * j, pk);
+                if (redo) {
+                    float best[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        best[j] = __uint_as_float(v[j][0]);
+#pragma unroll
+                        for (int e = 1; e < 32; ++e) best[j] = fmaxf(best[j], __uint_as_float(v[j][e]));
+                    }
+                    const float mt = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * a.scale;
+                    const float mn = fmaxf(m, mt);
+                    if (c > 0) {
+                        // the slot's product before these scores has been added to O
+                        const float f = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
+                        l *= f;
+#pragma unroll 1
+                        for (int cc = 0; cc < D; cc += 16) {
+                            float acc[16];
+                            uint32_t w[16];
+                            tmem_ld16(tO + cc, acc);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(acc[e] * f);
+                            tmem_st16(tO + cc, w);
+                        }
+                    }
+                    m = mn;
+                    begin();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) exps(j);
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tmem_wait_st();
             }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            tmem_wait_st();
-        }
-        ++cs;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[t]);
-        if (o.last()) {
-            // the epilogue has read the slot's previous (m, l)
-            if (on > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait_suspend(&bars->o_free[t], (on - 1) & 1u, x.abort_flag));
-                if (!ok) break;
-            }
-            ++on;
-            ml[row] = make_float2(m, l);
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->den_full[t]);
+            if (lane == 0) mbar_arrive(&bars->p_full[t]);
         }
+        if (!ok) break;
+        // the epilogue has read the slot's previous (m, l)
+        if (on > 0) {
+            ok = x.wait(&bars->o_free[t], on - 1);
+            if (!ok) break;
+        }
+        ++on;
+        ml[row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->den_full[t]);
     }
     if (!ok && lane == 0) x.give_up();
 }
 
 // One row tile out: acc = f0 O_s0 + f1 O_s1 (the second slot only with `both`).
 template <int D>
-__device__ __forceinline__ bool put_tile(const Ctx<D>& x, const TcArgs& a, const Seg& g, int tile, int s0, bool both,
+__device__ __forceinline__ bool put_tile(const Ctx<D>& x, const TcArgs& a, const Item& g, int tile, int s0, bool both,
                                          unsigned (&on)[2], int quad, int lane) {
     using C = Cfg<D>;
     auto* bars = x.bars;
@@ -520,7 +647,7 @@ __device__ __forceinline__ bool put_tile(const Ctx<D>& x, const TcArgs& a, const
         f1 *= rcp;
         if (mine) {
             const int i = (g.row0 + r) / a.s.g, hq = g.h * a.s.g + (g.row0 + r - i * a.s.g);
-            const int64_t tok = a.s.first_row(g.b) + i;
+            const int64_t tok = g.first + i;
             out = a.O + tok * a.o_t + (int64_t)hq * a.o_h;
             if (a.lse) a.lse[tok * (a.s.Hkv * a.s.g) + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
@@ -563,21 +690,25 @@ __device__ __forceinline__ bool put_tile(const Ctx<D>& x, const TcArgs& a, const
 }
 
 template <int D>
-__device__ __forceinline__ void role_epilogue(const Ctx<D>& x, const TcArgs& a, int quad, int lane, int64_t total,
-                                              int active) {
+__device__ __forceinline__ void role_epilogue(const Ctx<D>& x, const TcArgs& a, int quad, int lane) {
     unsigned on[2] = {0, 0};
+    unsigned k0 = 0;
     bool ok = true;
     int4 join = make_int4(0, 0, 0, -1);
-    Ops o;
-    o.start(a, x.lo, x.hi);
-    for (; o.valid && ok; o.next_seg(a)) {
-        const int s0 = (int)(o.k0 & 1u);
-        if (o.two)
-            ok = put_tile<D>(x, a, o.g, 0, s0, false, on, quad, lane) &&
-                 put_tile<D>(x, a, o.g, 1, s0 ^ 1, false, on, quad, lane);
-        else
-            ok = put_tile<D>(x, a, o.g, 0, s0, o.n > 1, on, quad, lane);
-        if (o.g.t0 > 0 && o.g.t1 == o.g.nt) join = make_int4(o.g.b, o.g.h, o.g.t, block_of(total, active, o.g.unit_start));
+    for (unsigned s = 0; ok; ++s) {
+        ok = x.item_wait(s);
+        if (!ok) break;
+        const Item g = *x.item(s);
+        x.item_done(s, lane);
+        if (g.t1 == g.t0) break;
+        const int s0 = (int)(k0 & 1u), n = g.t1 - g.t0;
+        if (g.rows > a.R) {
+            ok = put_tile<D>(x, a, g, 0, s0, false, on, quad, lane) && put_tile<D>(x, a, g, 1, s0 ^ 1, false, on, quad, lane);
+        } else {
+            ok = put_tile<D>(x, a, g, 0, s0, n > 1, on, quad, lane);
+            k0 += n;
+        }
+        if (g.join >= 0) join = make_int4(g.b, g.h, g.t, g.join);
     }
     if (!ok && lane == 0) x.give_up();
     if (quad == 0 && lane == 0) a.p.joins[blockIdx.x] = join;
@@ -588,13 +719,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcArgs a) {
     using C = Cfg<D>;
-    constexpr int NS = C::NS;
     extern __shared__ __align__(1024) unsigned char sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Ctx<D> x;
     x.sm = sm;
     x.sbase = smem_u32(sm);
-    x.bars = reinterpret_cast<Bars<NS>*>(sm + C::off_bar);
+    x.bars = reinterpret_cast<Bars<C::NK, C::NV>*>(sm + C::off_bar);
     x.abort_flag = &x.bars->abort;
     auto* bars = x.bars;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -604,15 +734,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->q_free[t], 1);
             mbar_init(&bars->s_full[t], 1);
             mbar_init(&bars->p_full[t], 4);  // one arrival per warp of the softmax group
-            mbar_init(&bars->pv_done[t], 1);
             mbar_init(&bars->o_full[t], 1);
             mbar_init(&bars->o_free[t], 4);  // one arrival per warp of the epilogue group
             mbar_init(&bars->den_full[t], 4);
         }
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->fixed[s], 1);
-            mbar_init(&bars->empty[s], 2);  // the tensor cores' last use, and warp 2
+        for (int s = 0; s < C::NK; ++s) {
+            mbar_init(&bars->k_full[s], 1);
+            mbar_init(&bars->k_empty[s], 1);
+        }
+        for (int s = 0; s < C::NV; ++s) {
+            mbar_init(&bars->v_full[s], 1);
+            mbar_init(&bars->v_fixed[s], 1);
+            mbar_init(&bars->v_empty[s], 1);
+        }
+        for (int s = 0; s < kItems; ++s) {
+            mbar_init(&bars->item_full[s], 1);
+            mbar_init(&bars->item_empty[s], kItemReaders);
         }
         mbar_init(&bars->drain, 1);
         // the operand layouts need a 1024-byte aligned base
@@ -636,23 +773,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t total = a.p.prefix[a.s.B];
     const int active = active_blocks(total, a.G), c = blockIdx.x;
-    x.lo = c < active ? block_start(total, active, c) : 0;
-    x.hi = c < active ? block_start(total, active, c + 1) : 0;
+    const int64_t lo = c < active ? block_start(total, active, c) : 0, hi = c < active ? block_start(total, active, c + 1) : 0;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (go) {
-            if (warp == 0) role_producer<D>(x, a, &tmQ, &tmK, &tmV, lane);
-            else if (warp == 1 && lane == 0) role_mma<D>(x, a);
-            else if (warp == 2) role_fix<D>(x, a, lane);
+            if (warp == 0) role_copy<D, false>(x, a, &tmQ, &tmK, lane);
+            else if (warp == 1) role_mma<D>(x, a, lane);
+            else if (warp == 2) role_plan<D>(x, a, lane, lo, hi, total, active);
+            else role_copy<D, true>(x, a, &tmQ, &tmV, lane);
         }
         __syncwarp();
     } else if (warp < 12) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        if (go) role_softmax<D>(x, a, (warp - 4) >> 2, warp & 3, lane);
+        if (go) role_softmax<D>(x, a, (unsigned)(warp - 4) >> 2, warp & 3, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsEpilogue));
-        if (go) role_epilogue<D>(x, a, warp & 3, lane, total, active);
+        if (go) role_epilogue<D>(x, a, warp & 3, lane);
         else if (warp == 12 && lane == 0) a.p.joins[c] = make_int4(0, 0, 0, -1);
     }
 

@@ -89,6 +89,21 @@ __device__ __forceinline__ bool mbar_wait(void* mbar, unsigned parity,
     }
 }
 
+// One lane of a whole warp, the same each time.  Instructions that take their
+// operands from uniform registers (tcgen05.mma, TMA copies) are issued under
+// this: under a lane comparison the compiler wraps each in a loop over lanes.
+__device__ __forceinline__ bool elect_one() {
+    unsigned one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(one)
+        :
+        : "memory");
+    return one != 0;
+}
+
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
