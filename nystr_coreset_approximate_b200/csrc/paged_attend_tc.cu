@@ -6,32 +6,35 @@
 // (R = floor(128 / g) g), loaded by one TMA box that gathers the g heads; a
 // unit has up to two of them.  The work is a sequence of operations, numbered
 // k = 0, 1, ...; operation k takes one row tile and one tile of 128 keys in slot
-// k & 1 of the tensor memory (scores S, accumulator O):
+// k & 1 (a softmax group, and P and O in tensor memory):
 //     S = Q K^T          (tcgen05.mma, both operands in shared memory)
-//     P = 2^(beta log2e S - m), rounded to bf16, written over S
+//     P = 2^(beta log2e S - m), rounded to bf16
 //     O += P V           (A from tensor memory, V as it lies: keys by columns)
 // A unit with two row tiles runs both against each key tile (one slot each, one
 // load of K and V for 2 R rows: the tensor cores bound it); a unit with one, a
 // decoded token's or a short chunk's, runs successive key tiles in the two slots
 // with a running maximum and sum of its own for each (HBM bounds it), which the
-// epilogue adds up.  The issue order is S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...,
-// across units: while one slot's scores are exponentiated the other's products
-// run, and S(k + 2) may overwrite P(k), which PV(k) has read (products run in
-// issue order).  Warp roles:
-//   warp 0      copies K tiles: page lookups (one lane per page) and TMA
-//   warp 1      tensor cores.  All of its code is on the path between two
-//               products, so it keeps only counters
-//   warp 2      cuts the block's share into segments (one unit's key tiles) and
-//               hands them to the other roles through a ring; follows the V
-//               tiles and zeroes their rows at or past the request's length:
-//               what the page holds there may be NaN, and 0 NaN is NaN
+// epilogue adds up.  S(k) waits for the scores of k - 1 to be taken, PV(k) for P(k),
+// across units.  The slots share one place for scores: a group takes its scores
+// into registers at once (128 of a thread's), which frees it for the other
+// slot's next product, so that S(k + 2) does not wait for P(k) and both groups
+// exponentiate without a pause.  Warp roles:
+//   warp 0      cuts the block's share into segments (one unit's key tiles), hands
+//               them to the other roles through a ring, and copies K tiles: page
+//               lookups (one lane per page) and TMA
+//   warp 1      tensor cores, one thread: S(k + 2), then PV(k).  The tensor pipe
+//               holds only a few products and runs dry when the code between two
+//               issues is long; two issuing warps are no way out, products of both
+//               kinds in turn run at half the rate
+//   warp 2      follows the V tiles and zeroes their rows at or past the request's
+//               length: what the page holds there may be NaN, and 0 NaN is NaN
 //   warp 3      copies Q and V tiles
 //   warps 4-7   softmax of slot 0, warps 8-11 of slot 1, one row per thread.  The
 //               exponentials are formed with the maximum of the tiles before;
-//               only when a row's grows by more than 2^8 is it raised, O rescaled
-//               and the tile done again (sums in float32 hold 2^8, and a bf16 P is
-//               as exact there as at 1), so that the tile's maximum is not on the
-//               path from S to P
+//               only when a row's sum over the tile says that it has grown far is
+//               the maximum raised, O rescaled and the tile done again (float32
+//               sums hold 2^16, and a bf16 P is as exact there as at 1), so that
+//               the tile's maximum is not on the path from S to P
 //   warps 12-15 epilogue: O / l as bf16, or a partial sum of a unit that is cut
 // P is rounded to bf16 for the product (the operand type of V); the sum l is
 // float32 of the unrounded P.
@@ -67,6 +70,7 @@ static_assert(kRegsLow + 2 * kRegsSoftmax + kRegsEpilogue == 512, "register spli
 constexpr unsigned long long kDrainNs = 100000000ull;
 constexpr int kItems = 8;  // segments in the ring
 constexpr int kLead = 5;   // segments that warp 2 hands out ahead of its own
+constexpr float kRaise = 65536.f;  // a row's sum of one tile above which its maximum is raised
 constexpr int kAhead = 3;  // key tiles between the first touch of their page ids and their use
 
 // One segment: key tiles [t0, t1) of a unit; t1 == t0 ends the ring.
@@ -78,7 +82,7 @@ template <int NK, int NV>
 struct Bars {
     uint64_t q_full[2], q_free[2];
     uint64_t k_full[NK], k_empty[NK], v_full[NV], v_fixed[NV], v_empty[NV];
-    uint64_t s_full[2], p_full[2], o_full[2], o_free[2], den_full[2];
+    uint64_t s_go, s_full[2], p_full[2], pv_done[2], o_full[2], o_free[2], den_full[2];
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t drain;
     unsigned tmem_base;
@@ -102,7 +106,9 @@ struct Cfg {
     static constexpr uint32_t total = off_bar + (uint32_t)sizeof(Bars<NK, NV>);
     static constexpr unsigned tmem_cols = 512;
     static constexpr unsigned col_O = 0;      // O of slot t at t * D
-    static constexpr unsigned col_S = 2 * D;  // S of slot t at 2 D + 128 t
+    static constexpr unsigned col_S = 2 * D;  // S
+    static constexpr unsigned col_P = 2 * D + kKeys;  // P of slot t, two bf16 to a column, at col_P + 64 t
+    static_assert(col_P + kKeys <= tmem_cols, "tensor memory");
     static_assert(total <= 232448, "shared memory");
 };
 
@@ -131,21 +137,21 @@ struct Ctx {
     __device__ __forceinline__ bool wait(uint64_t* b, unsigned parity) const {
         return __all_sync(0xffffffffu, mbar_wait_suspend(b, parity & 1u, abort_flag));
     }
+    __device__ __forceinline__ bool wait_one(uint64_t* b, unsigned parity) const {
+        return mbar_wait_suspend(b, parity & 1u, abort_flag);
+    }
     __device__ __forceinline__ Item* item(unsigned s) const {
         return reinterpret_cast<Item*>(sm + Cfg<D>::off_items) + s % kItems;
     }
     // segment s once it is in the ring
     __device__ __forceinline__ bool item_wait(unsigned s) const { return wait(&bars->item_full[s % kItems], s / kItems); }
-    __device__ __forceinline__ bool item_there(unsigned s) const {
-        return __all_sync(0xffffffffu, mbar_try(smem_u32(&bars->item_full[s % kItems]), (s / kItems) & 1u));
-    }
     // this warp has read segment s
     __device__ __forceinline__ void item_done(unsigned s, int lane) const {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->item_empty[s % kItems]);
     }
 };
-constexpr int kItemReaders = 3 + 8 + 4;  // warps 0, 1, 3, the softmax groups, the epilogue
+constexpr int kItemReaders = 4 + 8 + 4;  // warps 0 to 3, the softmax groups, the epilogue
 
 // A place in a ring of N stages and the parity of its use.
 template <int N>
@@ -218,10 +224,11 @@ __device__ __forceinline__ void copy_tile(const TcArgs& a, const CUtensorMap* tm
     }
 }
 
-// Warps 0 and 3: the K tiles (V false), or each segment's Q tiles and its V tiles.
+// Warps 0 and 3: the segments and the K tiles (V false), or each segment's Q tiles
+// and its V tiles.
 template <int D, bool V>
 __device__ __forceinline__ void role_copy(const Ctx<D>& x, const TcArgs& a, const CUtensorMap* tmQ, const CUtensorMap* tm,
-                                          int lane) {
+                                          int lane, int64_t lo, int64_t hi, int64_t total, int active) {
     using C = Cfg<D>;
     constexpr int N = V ? C::NV : C::NK;
     auto* bars = x.bars;
@@ -235,7 +242,31 @@ __device__ __forceinline__ void role_copy(const Ctx<D>& x, const TcArgs& a, cons
     Ring<N> r;
     unsigned n = 0, qn = 0;  // tiles and row tiles issued
     bool ok = true;
+    Walk<kKeys> w;
+    unsigned pushed = 0;
+    bool more = !V;
+    if (!V) w.start(a.s, a.p, lo, hi);
     for (unsigned s = 0; ok; ++s) {
+        while (more && pushed < s + kLead && ok) {
+            if (pushed >= kItems) ok = x.wait(&bars->item_empty[pushed % kItems], pushed / kItems - 1);
+            if (!ok) break;
+            Seg g;
+            more = w.next(a.s, g);
+            if (lane == 0) {
+                Item* it = x.item(pushed);
+                if (more) {
+                    const bool ends = g.t0 > 0 && g.t1 == g.nt;  // the last piece of a cut unit
+                    *it = Item{g.b, g.h, g.t, g.n, g.L, g.row0, g.rows, g.t0, g.t1, g.nt, a.s.first_row(g.b),
+                               ends ? block_of(total, active, g.unit_start) : -1};
+                } else {
+                    it->t0 = it->t1 = 0;
+                }
+                mbar_arrive(&bars->item_full[pushed % kItems]);
+            }
+            __syncwarp();
+            ++pushed;
+        }
+        if (!ok) break;
         ok = x.item_wait(s);
         if (!ok) break;
         const Item g = *x.item(s);
@@ -279,61 +310,6 @@ __device__ __forceinline__ void role_copy(const Ctx<D>& x, const TcArgs& a, cons
     }
 }
 
-// Warp 2.
-template <int D>
-__device__ __forceinline__ void role_plan(const Ctx<D>& x, const TcArgs& a, int lane, int64_t lo, int64_t hi, int64_t total,
-                                          int active) {
-    using C = Cfg<D>;
-    auto* bars = x.bars;
-    Walk<kKeys> w;
-    w.start(a.s, a.p, lo, hi);
-    Ring<C::NV> r;
-    unsigned pushed = 0;
-    bool more = true, ok = true;
-    for (unsigned s = 0; ok; ++s) {
-        while (more && pushed < s + kLead && ok) {
-            if (pushed >= kItems) ok = x.wait(&bars->item_empty[pushed % kItems], pushed / kItems - 1);
-            if (!ok) break;
-            Seg g;
-            more = w.next(a.s, g);
-            if (lane == 0) {
-                Item* it = x.item(pushed);
-                if (more) {
-                    const bool ends = g.t0 > 0 && g.t1 == g.nt;  // the last piece of a cut unit
-                    *it = Item{g.b, g.h, g.t, g.n, g.L, g.row0, g.rows, g.t0, g.t1, g.nt, a.s.first_row(g.b),
-                               ends ? block_of(total, active, g.unit_start) : -1};
-                } else {
-                    it->t0 = it->t1 = 0;
-                }
-                mbar_arrive(&bars->item_full[pushed % kItems]);
-            }
-            __syncwarp();
-            ++pushed;
-        }
-        if (!ok) break;
-        const Item* it = x.item(s);
-        const int t0 = it->t0, t1 = it->t1, L = it->L;
-        __syncwarp();
-        if (t0 == t1) break;
-        for (int kt = t0; kt < t1; ++kt, r.next()) {
-            ok = x.wait(&bars->v_full[r.s], r.ph);
-            if (!ok) break;
-            if ((kt + 1) * kKeys > L) {
-                const int keep = max(L - kt * kKeys, 0);
-                unsigned char* tile = x.sm + C::off_v + (unsigned)r.s * C::t_bytes;
-                for (int e = lane; e < (kKeys - keep) * 8; e += 32)
-#pragma unroll
-                    for (int kb = 0; kb < C::KB; ++kb)
-                        *reinterpret_cast<uint4*>(tile + kb * C::blk + keep * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-                fence_async_smem();
-                __syncwarp();
-            }
-            if (lane == 0) mbar_arrive(&bars->v_fixed[r.s]);
-        }
-    }
-    if (!ok && lane == 0) x.give_up();
-}
-
 // S_t = Q K^T and O_t (+)= P_t V, one thread.
 template <int D>
 __device__ __forceinline__ void gemm_s(unsigned tmem_s, uint32_t q_lo, uint32_t k_lo, uint32_t hi) {
@@ -353,125 +329,184 @@ __device__ __forceinline__ void gemm_pv(unsigned tmem_o, unsigned tmem_p, uint32
 
 // The operations of a segment as warp 1 sees them.
 struct OpCursor {
-    unsigned s;   // segment
-    int i, n;     // operation of n
-    bool two, valid;
+    unsigned s = 0;  // segment
+    int i, n;        // operation of n
+    bool two;
     __device__ __forceinline__ bool opens() const { return !two || !(i & 1); }  // first use of the key tile
     __device__ __forceinline__ bool closes() const { return !two || (i & 1); }  // last use
     __device__ __forceinline__ bool q_opens() const { return i < (two ? 2 : 1); }
     __device__ __forceinline__ bool q_closes() const { return i >= n - (two ? 2 : 1); }
     __device__ __forceinline__ bool first() const { return i < 2; }  // of its slot in the segment
     __device__ __forceinline__ bool last() const { return i >= n - 2; }
+    // the segment s; n = 0 after the last
     template <int D>
     __device__ __forceinline__ bool load(const Ctx<D>& x, int R) {
-        if (!x.item_wait(s)) return false;
+        if (!x.wait_one(&x.bars->item_full[s % kItems], s / kItems)) return false;
         const Item* it = x.item(s);
         two = it->rows > R;
         n = (it->t1 - it->t0) << (two ? 1 : 0);
         i = 0;
-        valid = n > 0;
         return true;
     }
 };
 
-// Warp 1.  All lanes walk alike, one issues.
+// Warp 1, one thread.
 template <int D>
-__device__ __forceinline__ void role_mma(const Ctx<D>& x, const TcArgs& a, int lane) {
+__device__ __forceinline__ void role_mma(const Ctx<D>& x, const TcArgs& a) {
     using C = Cfg<D>;
     auto* bars = x.bars;
     const uint64_t dk = umma_desc(x.sbase + C::off_k), dv = umma_desc_mn(x.sbase + C::off_v, C::blk);
     const uint32_t q_lo = (uint32_t)umma_desc(x.sbase + C::off_q), k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
     const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
-    Ring<C::NK> kr;  // the current K and V tile, and the next ones
+    Ring<C::NK> kr;
     Ring<C::NV> vr;
-    int ks = 0, vs = 0;
-    unsigned qn = 0;            // row tiles taken
-    unsigned q0 = 0;            // row tile of the S cursor's segment
-    unsigned kt = 0, vt = 0;    // slot of the next S and the next PV
-    unsigned pn[2] = {0, 0};    // operations of each slot
+    int ks = 0, vs = 0;         // stages of the current K and V tile
+    unsigned sn = 0, pn = 0;    // operations whose S, whose PV was issued
+    unsigned qn = 0, q0 = 0;    // row tiles taken; row tiles before the S cursor's segment
     unsigned on[2] = {0, 0};    // accumulations of each slot
-    bool ok;
     OpCursor k, v;
-    k.s = 0;
-    ok = k.load(x, a.R);
+    bool ok = k.load(x, a.R);
     v = k;
-    auto ready = [&]() {  // K, and Q, of the next S have arrived
+    auto scores = [&]() {
         if (k.opens()) {
             ks = kr.s;
-            if (!x.wait(&bars->k_full[kr.s], kr.ph)) return false;
+            if (!x.wait_one(&bars->k_full[kr.s], kr.ph)) return false;
             kr.next();
         }
         if (k.q_opens()) {
-            if (!x.wait(&bars->q_full[qn & 1u], qn / 2)) return false;
+            if (!x.wait_one(&bars->q_full[qn & 1u], qn / 2)) return false;
             ++qn;
         }
-        return true;
-    };
-    auto scores = [&]() {  // one thread
+        // the scores before are in registers
+        if (sn > 0 && !x.wait_one(&bars->s_go, sn - 1)) return false;
         const unsigned qb = (q0 + (k.two ? k.i & 1 : 0)) & 1u;
-        gemm_s<D>(x.tmem + C::col_S + kt * kKeys, q_lo + qb * (C::q_bytes >> 4), k_lo + (uint32_t)ks * (C::t_bytes >> 4), k_hi);
-        mma_commit(&bars->s_full[kt]);
+        tc_fence_after();
+        gemm_s<D>(x.tmem + C::col_S, q_lo + qb * (C::q_bytes >> 4), k_lo + (uint32_t)ks * (C::t_bytes >> 4), k_hi);
+        mma_commit(&bars->s_full[sn & 1u]);
         if (k.closes()) mma_commit(&bars->k_empty[ks]);
         if (k.q_closes()) mma_commit(&bars->q_free[qb]);
-    };
-    auto next_k = [&]() {
-        kt ^= 1u;
+        ++sn;
         if (++k.i == k.n) {
             q0 += k.two ? 2 : 1;
             ++k.s;
-            ok = k.load(x, a.R);
+            return k.load(x, a.R);
         }
+        return true;
     };
-    for (int e = 0; e < 2 && ok && k.valid; ++e) {
-        ok = ready();
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) scores();
-        __syncwarp();
-        next_k();
-    }
-    while (ok && v.valid) {
-        const unsigned t = vt;
-        if (v.opens()) {
+    // Both cursors inside one segment of two row tiles: the same without its conditions, a
+    // key tile at a time.  The code of the general form between two products takes longer
+    // than they do.
+    auto pairs = [&]() {
+        const unsigned t0 = pn & 1u;
+        const uint32_t qa = q_lo + (q0 & 1u) * (C::q_bytes >> 4), qb = q_lo + (~q0 & 1u) * (C::q_bytes >> 4);
+        const unsigned o0 = x.tmem + C::col_O + t0 * D, o1 = x.tmem + C::col_O + (t0 ^ 1u) * D;
+        const unsigned p0 = x.tmem + C::col_P + t0 * (kKeys / 2), p1 = x.tmem + C::col_P + (t0 ^ 1u) * (kKeys / 2);
+        uint64_t *s_full0 = &bars->s_full[t0], *s_full1 = &bars->s_full[t0 ^ 1u];
+        uint64_t *p_full0 = &bars->p_full[t0], *p_full1 = &bars->p_full[t0 ^ 1u];
+        uint64_t *pv_done0 = &bars->pv_done[t0], *pv_done1 = &bars->pv_done[t0 ^ 1u];
+        unsigned par0 = pn / 2, par1 = (pn + 1) / 2;
+        unsigned go = sn - 1;
+        const int m = (k.n - 2 - k.i) / 2;
+        for (int e = 0; e < m; ++e) {
+            const uint32_t kd = k_lo + (uint32_t)kr.s * (C::t_bytes >> 4), vd = v_lo + (uint32_t)vr.s * (C::t_bytes >> 4);
+            if (!x.wait_one(&bars->k_full[kr.s], kr.ph) || !x.wait_one(&bars->s_go, go)) return false;
+            tc_fence_after();
+            gemm_s<D>(x.tmem + C::col_S, qa, kd, k_hi);
+            mma_commit(s_full0);
+            if (!x.wait_one(&bars->v_fixed[vr.s], vr.ph) || !x.wait_one(p_full0, par0)) return false;
+            tc_fence_after();
+            gemm_pv<D>(o0, p0, vd, v_hi, false);
+            mma_commit(pv_done0);
+            if (!x.wait_one(&bars->s_go, go + 1)) return false;
+            tc_fence_after();
+            gemm_s<D>(x.tmem + C::col_S, qb, kd, k_hi);
+            mma_commit(s_full1);
+            mma_commit(&bars->k_empty[kr.s]);
+            if (!x.wait_one(p_full1, par1)) return false;
+            tc_fence_after();
+            gemm_pv<D>(o1, p1, vd, v_hi, false);
+            mma_commit(pv_done1);
+            mma_commit(&bars->v_empty[vr.s]);
+            kr.next();
+            vr.next();
+            go += 2;
+            ++par0;
+            ++par1;
+        }
+        k.i += 2 * m;
+        v.i += 2 * m;
+        sn += 2 * m;
+        pn += 2 * m;
+        return true;
+    };
+    for (int e = 0; e < 2 && ok && k.n > 0; ++e) ok = scores();
+    while (ok && v.n > 0) {
+        if (v.two && v.i == 2 && k.s == v.s && k.n - k.i > 2) {
+            ok = pairs();
+            if (!ok) break;
+        }
+        if (k.n > 0) ok = scores();
+        const unsigned t = pn & 1u;
+        if (ok && v.opens()) {
             vs = vr.s;
-            ok = x.wait(&bars->v_fixed[vr.s], vr.ph);
+            ok = x.wait_one(&bars->v_fixed[vr.s], vr.ph);
             vr.next();
         }
-        ok = ok && (!k.valid || ready());
         if (ok && v.first()) {  // the epilogue has taken the slot's previous O
-            if (on[t] > 0) ok = x.wait(&bars->o_free[t], on[t] - 1);
+            if (on[t] > 0) ok = x.wait_one(&bars->o_free[t], on[t] - 1);
             ++on[t];
         }
-        ok = ok && x.wait(&bars->p_full[t], pn[t]++);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-            gemm_pv<D>(x.tmem + C::col_O + t * D, x.tmem + C::col_S + t * kKeys, v_lo + (uint32_t)vs * (C::t_bytes >> 4), v_hi,
-                       v.first());
-            if (v.last()) mma_commit(&bars->o_full[t]);
-            if (v.closes()) mma_commit(&bars->v_empty[vs]);
-            // over the columns of P, which the product above has read by then
-            if (k.valid) scores();
+        if (!ok || !x.wait_one(&bars->p_full[t], pn / 2)) {
+            ok = false;
+            break;
         }
-        __syncwarp();
-        if (k.valid) next_k();
-        vt ^= 1u;
-        if (ok && ++v.i == v.n) {
-            x.item_done(v.s, lane);
+        tc_fence_after();
+        gemm_pv<D>(x.tmem + C::col_O + t * D, x.tmem + C::col_P + t * (kKeys / 2), v_lo + (uint32_t)vs * (C::t_bytes >> 4), v_hi,
+                   v.first());
+        mma_commit(&bars->pv_done[t]);
+        if (v.last()) mma_commit(&bars->o_full[t]);
+        if (v.closes()) mma_commit(&bars->v_empty[vs]);
+        ++pn;
+        if (++v.i == v.n) {
+            mbar_arrive(&bars->item_empty[v.s % kItems]);
             ++v.s;
             ok = v.load(x, a.R);
         }
     }
-    if (!ok && lane == 0) x.give_up();
-    if (elect_one()) mma_commit(&bars->drain);
-    __syncwarp();
+    if (!ok) x.give_up();
+    mma_commit(&bars->drain);
     mbar_wait(&bars->drain, 0, kDrainNs);
 }
 
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+// Warp 2.
+template <int D>
+__device__ __forceinline__ void role_tail(const Ctx<D>& x, int lane) {
+    using C = Cfg<D>;
+    Ring<C::NV> r;
+    bool ok = true;
+    for (unsigned s = 0; ok; ++s) {
+        ok = x.item_wait(s);
+        if (!ok) break;
+        const int t0 = x.item(s)->t0, t1 = x.item(s)->t1, L = x.item(s)->L;
+        x.item_done(s, lane);
+        if (t0 == t1) break;
+        for (int kt = t0; kt < t1; ++kt, r.next()) {
+            ok = x.wait(&x.bars->v_full[r.s], r.ph);
+            if (!ok) break;
+            if ((kt + 1) * kKeys > L) {
+                const int keep = max(L - kt * kKeys, 0);
+                unsigned char* tile = x.sm + C::off_v + (unsigned)r.s * C::t_bytes;
+                for (int e = lane; e < (kKeys - keep) * 8; e += 32)
+#pragma unroll
+                    for (int kb = 0; kb < C::KB; ++kb)
+                        *reinterpret_cast<uint4*>(tile + kb * C::blk + keep * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(&x.bars->v_fixed[r.s]);
+        }
+    }
+    if (!ok && lane == 0) x.give_up();
 }
 
 // Softmax of slot t: thread `row` owns row `row` of the slot's row tile.
@@ -480,7 +515,8 @@ __device__ __forceinline__ void role_softmax(const Ctx<D>& x, const TcArgs& a, u
     using C = Cfg<D>;
     auto* bars = x.bars;
     const int row = quad * 32 + lane;
-    const unsigned tS = x.tmem + C::col_S + t * kKeys + ((unsigned)(quad * 32) << 16);
+    const unsigned tS = x.tmem + C::col_S + ((unsigned)(quad * 32) << 16);
+    const unsigned tP = x.tmem + C::col_P + t * (kKeys / 2) + ((unsigned)(quad * 32) << 16);
     const unsigned tO = x.tmem + C::col_O + t * D + ((unsigned)(quad * 32) << 16);
     float2* ml = reinterpret_cast<float2*>(x.sm + C::off_ml) + t * kRows;
     const float2 a2 = make_float2(a.scale, a.scale);
@@ -511,59 +547,55 @@ __device__ __forceinline__ void role_softmax(const Ctx<D>& x, const TcArgs& a, u
         for (int c = 0; c < ops; ++c, lim -= step) {
             ok = x.wait(&bars->s_full[t], cs);
             if (!ok) break;
-            ++cs;
             tc_fence_after();
+            uint32_t v[4][32];
             if (active) {
-                const bool edge = __any_sync(0xffffffffu, lim < kKeys);
-                uint32_t v[4][32];
-                float2 sum[2], nb;
-                uint32_t top;
-                auto mask = [&](int j) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * j + e >= lim) v[j][e] = 0xff800000u;
-                };
-                auto begin = [&]() {
+                for (int j = 0; j < 4; ++j) tmem_ld32_nowait(tS + 32 * j, v[j]);
+                tmem_wait_ld();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->s_go);
+            // the slot's product before has read P, and been added to O
+            if (cs > 0) {
+                ok = x.wait(&bars->pv_done[t], cs - 1);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            ++cs;
+            if (active) {
+                if (__any_sync(0xffffffffu, lim < kKeys)) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * j + e >= lim) v[j][e] = 0xff800000u;
+                }
+                float sum;
+                auto exps = [&]() {  // P, and its sum
                     const float base = m == -INFINITY ? 0.f : m;
-                    nb = make_float2(-base, -base);
-                    sum[0] = sum[1] = make_float2(0.f, 0.f);
-                    top = 0u;
-                };
-                auto exps = [&](int j) {  // P of 32 keys
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 y =
-                            ffma2(make_float2(__uint_as_float(v[j][2 * e]), __uint_as_float(v[j][2 * e + 1])), a2, nb);
-                        const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
-                        pk[e] = pack_bf16x2(p0, p1);
-                        sum[e & 1] = fadd2(sum[e & 1], make_float2(p0, p1));
-                        top = max_bf16x2(top, pk[e]);
-                    }
-                    tmem_st16(tS + 16 * j, pk);
-                };
-                bool redo = c == 0;
-                if (c == 0) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) tmem_ld32_nowait(tS + 32 * j, v[j]);
-                    tmem_wait_ld();
-                    if (edge) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) mask(j);
-                    }
-                } else {
-                    begin();
-                    tmem_ld32_nowait(tS, v[0]);
+                    const float2 nb = make_float2(-base, -base);
+                    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        tmem_wait_ld();
-                        if (j < 3) tmem_ld32_nowait(tS + 32 * (j + 1), v[j + 1]);
-                        if (edge) mask(j);
-                        exps(j);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y =
+                                ffma2(make_float2(__uint_as_float(v[j][2 * e]), __uint_as_float(v[j][2 * e + 1])), a2, nb);
+                            const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                            pk[e] = pack_bf16x2(pr.x, pr.y);
+                            part[e & 1] = fadd2(part[e & 1], pr);
+                        }
+                        tmem_st16(tP + 16 * j, pk);
                     }
-                    // 2^8 in bf16 is 0x4380; P is not negative, so its bits order as numbers
-                    const bool high = (top & 0xffffu) > 0x4380u || (top >> 16) > 0x4380u;
-                    redo = __any_sync(0xffffffffu, high || (m == -INFINITY && lim > 0));
+                    sum = (part[0].x + part[0].y) + (part[1].x + part[1].y);
+                };
+                bool redo = c == 0;
+                if (c > 0) {
+                    exps();
+                    redo = __any_sync(0xffffffffu, sum > kRaise || (m == -INFINITY && lim > 0));
                 }
                 if (redo) {
                     float best[4];
@@ -576,7 +608,6 @@ __device__ __forceinline__ void role_softmax(const Ctx<D>& x, const TcArgs& a, u
                     const float mt = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * a.scale;
                     const float mn = fmaxf(m, mt);
                     if (c > 0) {
-                        // the slot's product before these scores has been added to O
                         const float f = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
                         l *= f;
 #pragma unroll 1
@@ -590,11 +621,9 @@ __device__ __forceinline__ void role_softmax(const Ctx<D>& x, const TcArgs& a, u
                         }
                     }
                     m = mn;
-                    begin();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) exps(j);
+                    exps();
                 }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                l += sum;
                 tmem_wait_st();
             }
             tc_fence_before();
@@ -733,7 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->q_full[t], 1);
             mbar_init(&bars->q_free[t], 1);
             mbar_init(&bars->s_full[t], 1);
-            mbar_init(&bars->p_full[t], 4);  // one arrival per warp of the softmax group
+            mbar_init(&bars->pv_done[t], 1);
+            mbar_init(&bars->p_full[t], 4);  // the warps of the softmax group
             mbar_init(&bars->o_full[t], 1);
             mbar_init(&bars->o_free[t], 4);  // one arrival per warp of the epilogue group
             mbar_init(&bars->den_full[t], 4);
@@ -751,6 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->item_full[s], 1);
             mbar_init(&bars->item_empty[s], kItemReaders);
         }
+        mbar_init(&bars->s_go, 4);  // the warps that took the scores
         mbar_init(&bars->drain, 1);
         // the operand layouts need a 1024-byte aligned base
         bars->abort = (x.sbase & 1023u) ? 1 : 0;
@@ -778,10 +809,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (go) {
-            if (warp == 0) role_copy<D, false>(x, a, &tmQ, &tmK, lane);
-            else if (warp == 1) role_mma<D>(x, a, lane);
-            else if (warp == 2) role_plan<D>(x, a, lane, lo, hi, total, active);
-            else role_copy<D, true>(x, a, &tmQ, &tmV, lane);
+            if (warp == 0) role_copy<D, false>(x, a, &tmQ, &tmK, lane, lo, hi, total, active);
+            else if (warp == 1) {
+                if (elect_one()) role_mma<D>(x, a);
+                __syncwarp();
+            }
+            else if (warp == 2) role_tail<D>(x, lane);
+            else role_copy<D, true>(x, a, &tmQ, &tmV, lane, lo, hi, total, active);
         }
         __syncwarp();
     } else if (warp < 12) {
