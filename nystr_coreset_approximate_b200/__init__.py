@@ -160,10 +160,16 @@ def _check(status: int):
 
 
 # --------------------------------------------------------------------------- helpers
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -549,21 +555,50 @@ def forward_ex_host(Q_host, K_host, V_host, beta: float, r: int, seed: int = 0, 
 
 
 # --------------------------------------------------------------------------- exact cache in pages
-def _rows(t, name, dims, dtype=None):
-    """Pointer of a strided CUDA tensor whose last dimension is contiguous."""
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
+# These calls stand in a decoding step, where the time to issue them counts: the
+# current device and stream are read once, and each tensor is looked at once.
+def _device(t, name) -> int:
+    """The current device; `t` is the call's first tensor."""
+    if not t.is_cuda:
+        _not_here(t, name, None)
+    return _torch()._C._cuda_getDevice()
+
+
+def _raw_stream(stream, device: int) -> int:
+    """The cudaStream_t of `stream`, or of the current one on `device`."""
+    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(device)
+
+
+def _not_here(t, name, device):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    cur = _torch().cuda.current_device()
-    if t.device.index != cur:
-        raise ValueError(f"{name} is on cuda:{t.device.index} but the current device is cuda:{cur}; "
-                         f"call under torch.cuda.device({t.device.index})")
-    if dtype is not None and t.dtype != dtype:
+    raise ValueError(f"{name} is on cuda:{t.device.index} but the current device is cuda:{device}; "
+                     f"call under torch.cuda.device({t.device.index})")
+
+
+def _rows(t, name, dims, device, dtype):
+    """(pointer, strides) of a strided CUDA tensor whose last dimension is contiguous."""
+    strides = t.stride()
+    if len(strides) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    if strides[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if t.get_device() != device:
+        _not_here(t, name, device)
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    return _vp(t.data_ptr())
+    return t.data_ptr(), strides
+
+
+def _flat(t, name, device, dtype):
+    """Pointer of a contiguous CUDA tensor."""
+    if t.get_device() != device:
+        _not_here(t, name, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    return t.data_ptr()
 
 
 def _empty(shape, dtype, device, stream):
@@ -577,17 +612,21 @@ def _empty(shape, dtype, device, stream):
 
 
 def _shape_is(t, name, *shape):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
 
 
 def _pool(k_pool, v_pool):
-    """(pages, Hkv, page_size, d) of a pair of pools, and their strides {page, head, row}."""
-    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
+    """(pages, Hkv, page_size, d) of a pair of pools."""
+    shape = k_pool.shape
+    if len(shape) != 4 or shape != v_pool.shape:
         raise ValueError("k_pool and v_pool must both be [pages, Hkv, page_size, d]")
     if k_pool.dtype != v_pool.dtype:
         raise TypeError("k_pool and v_pool must share a dtype")
-    return k_pool.shape, (_i64 * 3)(*k_pool.stride()[:3]), (_i64 * 3)(*v_pool.stride()[:3])
+    return shape
+
+
+_Strides3 = _i64 * 3
 
 
 def page_tables(ctx_lens, new_lens, block_table, free_ring, ring_state, page_size: int, max_tokens: int, *,
@@ -611,55 +650,59 @@ def page_tables(ctx_lens, new_lens, block_table, free_ring, ring_state, page_siz
     _shape_is(new_lens, "new_lens", B)
     if ring_state.numel() < 2:
         raise ValueError("ring_state must hold (first free place, free pages)")
+    page_size, max_tokens = int(page_size), int(max_tokens)
     if max_tokens < 0:
         raise ValueError("max_tokens must be >= 0")
     W = block_table.shape[1]
-    # one allocation for the five outputs (each begins on a 16-byte boundary)
-    sizes = [B, B + 1, max_tokens, max_tokens, 4]
-    flat = _empty(sum(-(-n // 4) * 4 for n in sizes), i32, ctx_lens.device, stream)
-    outs, at = [], 0
-    for n in sizes:
-        outs.append(flat[at:at + n])
-        at += -(-n // 4) * 4
-    seq_lens, cu_new, positions, slots, ring_out = outs
+    dev = _device(ctx_lens, "ctx_lens")
+    ctx, new, table = (_flat(ctx_lens, "ctx_lens", dev, i32), _flat(new_lens, "new_lens", dev, i32),
+                       _rows(block_table, "block_table", 2, dev, i32)[0])
+    ring, state = _flat(free_ring, "free_ring", dev, i32), _flat(ring_state, "ring_state", dev, i32)
+    # one allocation for the five outputs
+    outs = _empty(2 * B + 2 * max_tokens + 5, i32, ctx_lens.device, stream)
+    seq = outs.data_ptr()
+    cu = seq + 4 * B
+    pos = cu + 4 * (B + 1)
+    slots = pos + 4 * max_tokens
     _check(lib().wildcat_page_tables(
-        _dev(ctx_lens, "ctx_lens", i32), _dev(new_lens, "new_lens", i32), B, _rows(block_table, "block_table", 2, i32),
-        block_table.stride(0) if B > 1 else max(W, 1), W, _dev(free_ring, "free_ring", i32), free_ring.numel(),
-        _dev(ring_state, "ring_state", i32), int(page_size), int(max_tokens), _dev(seq_lens, "seq_lens"),
-        _dev(cu_new, "cu_new"), _dev(positions, "positions"), _dev(slots, "slots"), _dev(ring_out, "ring_out"),
-        _stream(stream)))
-    return seq_lens, cu_new, positions, slots, ring_out
+        ctx, new, B, table, block_table.stride(0) if B > 1 else max(W, 1), W, ring, free_ring.numel(), state, page_size,
+        max_tokens, seq, cu, pos, slots, slots + 4 * max_tokens, _raw_stream(stream, dev)))
+    return outs.split_with_sizes((B, B + 1, max_tokens, max_tokens, 4))
 
 
-def _turn_args(positions, inv_freq, sections, T, d):
+def _turn_args(positions, inv_freq, sections, T, device):
     """(positions pointer, axis stride, inv_freq pointer, sections, axes) of the rotary calls."""
     torch = _torch()
     sections = [int(s) for s in sections]
+    axes = len(sections)
     if positions.dim() == 1:
         positions = positions[None]
     if positions.dim() != 2 or positions.shape[1] != T:
         raise ValueError("positions must be [axes, T], or [T] for one axis")
-    if positions.shape[0] != len(sections):
+    if positions.shape[0] != axes or axes < 1:
         raise ValueError("sections must name the pairs of each axis of positions")
     half = sum(sections)
     if inv_freq.dim() != 1 or inv_freq.shape[0] != half:
         raise ValueError(f"inv_freq must hold one frequency for each of the {half} pairs")
-    return (_rows(positions, "positions", 2, torch.int32), positions.stride(0), _dev(inv_freq, "inv_freq", torch.float64),
-            (_int * max(1, len(sections)))(*sections), len(sections))
+    pos, strides = _rows(positions, "positions", 2, device, torch.int32)
+    return (pos, strides[0], _flat(inv_freq, "inv_freq", device, torch.float64), (_int * axes)(*sections), axes)
 
 
 def _rotary(x, positions, inv_freq, sections, interleaved, backward, out, stream, name):
     if x.dim() != 3:
         raise ValueError(f"{name} must be [T, H, d]")
     T, H, d = x.shape
-    code = _dtype_code(x)
+    code, dtype, dev = _dtype_code(x), x.dtype, _device(x, name)
+    pos, pos_stride, freq, secs, axes = _turn_args(positions, inv_freq, sections, T, dev)
+    xp, xs = _rows(x, name, 3, dev, dtype)
     if out is None:
-        out = _empty((T, H, d), x.dtype, x.device, stream)
-    _shape_is(out, "out", T, H, d)
-    pos, pos_stride, freq, secs, axes = _turn_args(positions, inv_freq, sections, T, d)
-    _check(lib().wildcat_rotary(_rows(x, name, 3), x.stride(0), x.stride(1), code, T, H, d, pos, pos_stride, freq,
-                                secs, axes, int(bool(interleaved)), backward, _rows(out, "out", 3, x.dtype),
-                                out.stride(0), out.stride(1), _stream(stream)))
+        out = _empty((T, H, d), dtype, x.device, stream)
+        op, ot, oh = out.data_ptr(), H * d, d
+    else:
+        _shape_is(out, "out", T, H, d)
+        op, (ot, oh, _) = _rows(out, "out", 3, dev, dtype)
+    _check(lib().wildcat_rotary(xp, xs[0], xs[1], code, T, H, d, pos, pos_stride, freq, secs, axes,
+                                1 if interleaved else 0, backward, op, ot, oh, _raw_stream(stream, dev)))
     return out
 
 
@@ -690,37 +733,44 @@ def paged_write(k, v, slots, k_pool, v_pool, *, q=None, positions=None, inv_freq
     if k.dim() != 3 or k.shape != v.shape:
         raise ValueError("k and v must both be [T, Hkv, d]")
     T, Hkv, d = k.shape
-    (pages, heads, page_size, pd), ks, vs = _pool(k_pool, v_pool)
-    if (heads, pd) != (Hkv, d):
+    pages, heads, page_size, pd = _pool(k_pool, v_pool)
+    if heads != Hkv or pd != d:
         raise ValueError("k and the pools must have the same heads and head dim")
-    if not k.dtype == v.dtype == k_pool.dtype:
+    dtype = k.dtype
+    if dtype != v.dtype or dtype != k_pool.dtype:
         raise TypeError("k, v and the pools must share a dtype")
     _shape_is(slots, "slots", T)
+    code, dev = _dtype_code(k), _device(k, "k")
+    kp, (kt, kh, _) = _rows(k, "k", 3, dev, dtype)
+    vp, (vt, vh, _) = _rows(v, "v", 3, dev, dtype)
+    kpp, ks = _rows(k_pool, "k_pool", 4, dev, dtype)
+    vpp, vs = _rows(v_pool, "v_pool", 4, dev, dtype)
+    sp = _flat(slots, "slots", dev, torch.int32)
     pos = freq = secs = None
     pos_stride = axes = Hq = qt = qh = ot = oh = 0
     qp = op = None
     if positions is not None:
         if inv_freq is None or sections is None:
             raise ValueError("positions need inv_freq and sections")
-        pos, pos_stride, freq, secs, axes = _turn_args(positions, inv_freq, sections, T, d)
+        pos, pos_stride, freq, secs, axes = _turn_args(positions, inv_freq, sections, T, dev)
     if q is not None:
         if positions is None:
             raise ValueError("q is turned by positions: give them, or leave q out")
         if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d:
             raise ValueError("q must be [T, Hq, d]")
         Hq = q.shape[1]
+        qp, (qt, qh, _) = _rows(q, "q", 3, dev, dtype)
         if out is None:
-            out = _empty((T, Hq, d), q.dtype, q.device, stream)
-        _shape_is(out, "out", T, Hq, d)
-        qp, op = _rows(q, "q", 3, k.dtype), _rows(out, "out", 3, k.dtype)
-        qt, qh, ot, oh = q.stride(0), q.stride(1), out.stride(0), out.stride(1)
+            out = _empty((T, Hq, d), dtype, q.device, stream)
+            op, ot, oh = out.data_ptr(), Hq * d, d
+        else:
+            _shape_is(out, "out", T, Hq, d)
+            op, (ot, oh, _) = _rows(out, "out", 3, dev, dtype)
     elif out is not None:
         raise ValueError("out without q")
-    _check(lib().wildcat_paged_write(
-        _rows(k, "k", 3), k.stride(0), k.stride(1), _rows(v, "v", 3), v.stride(0), v.stride(1),
-        _dev(slots, "slots", torch.int32), _dtype_code(k), T, Hkv, d, _rows(k_pool, "k_pool", 4), ks,
-        _rows(v_pool, "v_pool", 4), vs, pages, page_size, pos, pos_stride, freq, secs, axes, int(bool(interleaved)),
-        qp, qt, qh, Hq, op, ot, oh, _stream(stream)))
+    _check(lib().wildcat_paged_write(kp, kt, kh, vp, vt, vh, sp, code, T, Hkv, d, kpp, _Strides3(*ks[:3]), vpp,
+                                     _Strides3(*vs[:3]), pages, page_size, pos, pos_stride, freq, secs, axes, 1 if interleaved else 0,
+                                     qp, qt, qh, Hq, op, ot, oh, _raw_stream(stream, dev)))
     return out
 
 
@@ -740,30 +790,38 @@ def paged_attend(q, k_pool, v_pool, block_table, seq_lens, cu_new, beta: float, 
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, d]")
     T, Hq, d = q.shape
-    (pages, Hkv, page_size, pd), ks, vs = _pool(k_pool, v_pool)
+    pages, Hkv, page_size, pd = _pool(k_pool, v_pool)
     if pd != d:
         raise ValueError("q and the pools must have the same head dim")
-    if q.dtype != k_pool.dtype:
+    dtype = q.dtype
+    if dtype != k_pool.dtype:
         raise TypeError("q and the pools must share a dtype")
     B = seq_lens.shape[0]
     _shape_is(cu_new, "cu_new", B + 1)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, W]")
-    if out is None:
-        out = _empty((T, Hq, d), q.dtype, q.device, stream)
-    _shape_is(out, "out", T, Hq, d)
     if lse is not None:
         _shape_is(lse, "lse", T, Hq)
+    code, dev = _dtype_code(q), _device(q, "q")
+    qp, (qt, qh, _) = _rows(q, "q", 3, dev, dtype)
+    kpp, ks = _rows(k_pool, "k_pool", 4, dev, dtype)
+    vpp, vs = _rows(v_pool, "v_pool", 4, dev, dtype)
+    table, rows = _rows(block_table, "block_table", 2, dev, i32)
+    lens, cu = _flat(seq_lens, "seq_lens", dev, i32), _flat(cu_new, "cu_new", dev, i32)
+    lp = None if lse is None else _flat(lse, "lse", dev, torch.float32)
+    if out is None:
+        out = _empty((T, Hq, d), dtype, q.device, stream)
+        op, ot, oh = out.data_ptr(), Hq * d, d
+    else:
+        _shape_is(out, "out", T, Hq, d)
+        op, (ot, oh, _) = _rows(out, "out", 3, dev, dtype)
     L = lib()
     W = block_table.shape[1]
-    nbytes = int(L.wildcat_paged_attend_workspace_size(B, d))
+    nbytes = L.wildcat_paged_attend_workspace_size(B, d)
     ws = _empty(nbytes, torch.uint8, q.device, stream)
-    _check(L.wildcat_paged_attend(
-        _rows(q, "q", 3), q.stride(0), q.stride(1), _rows(k_pool, "k_pool", 4), ks, _rows(v_pool, "v_pool", 4), vs,
-        pages, page_size, _dtype_code(q), T, Hq, Hkv, d, _rows(block_table, "block_table", 2, i32),
-        block_table.stride(0) if B > 1 else max(W, 1), W, _dev(seq_lens, "seq_lens", i32), _dev(cu_new, "cu_new", i32),
-        B, float(beta), int(bool(causal)), _rows(out, "out", 3, q.dtype), out.stride(0), out.stride(1),
-        _opt(lse, "lse", torch.float32), _dev(ws, "workspace"), nbytes, _stream(stream)))
+    _check(L.wildcat_paged_attend(qp, qt, qh, kpp, _Strides3(*ks[:3]), vpp, _Strides3(*vs[:3]), pages, page_size, code, T, Hq,
+                                  Hkv, d, table, rows[0] if B > 1 else max(W, 1), W, lens, cu, B, float(beta), 1 if causal else 0,
+                                  op, ot, oh, lp, ws.data_ptr(), nbytes, _raw_stream(stream, dev)))
     return out
 
 

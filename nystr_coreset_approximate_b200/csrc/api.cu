@@ -1029,7 +1029,7 @@ wildcat_status wildcat_paged_write(const void* k, int64_t k_token, int64_t k_hea
 
 size_t wildcat_paged_attend_workspace_size(int64_t B, int d) {
     if (B < 0 || d < 1) return 0;
-    return wildcat::paged_attend_workspace_bytes(B, d);
+    return wildcat::paged_attend_workspace_bytes(d);
 }
 
 wildcat_status wildcat_paged_attend(const void* Q, int64_t q_token, int64_t q_head, const void* k_pool,
@@ -1065,7 +1065,7 @@ wildcat_status wildcat_paged_attend(const void* Q, int64_t q_token, int64_t q_he
     for (const void* p : {Q, k_pool, v_pool, (const void*)O})
         if (!elem_aligned(p, dtype)) return bad(1, "%s: tensors must be aligned to their elements", who);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return bad(4, "%s: workspace must be 256-byte aligned", who);
-    if (ws_bytes < wildcat::paged_attend_workspace_bytes(B, d)) return bad(4, "%s: workspace too small", who);
+    if (ws_bytes < wildcat::paged_attend_workspace_bytes(d)) return bad(4, "%s: workspace too small", who);
     wildcat::PagedAttendRequest q{Q, q_token, q_head, k_pool, v_pool, pages, page_size, k_strides[0], k_strides[1],
                                   k_strides[2], v_strides[0], v_strides[1], v_strides[2], dtype, T, Hq, Hkv, d,
                                   block_table, table_stride, W, seq_lens, cu_new, B, beta, causal != 0, O, o_token,

@@ -243,7 +243,7 @@ struct PagedAttendRequest {
     void* ws;
     size_t ws_bytes;
 };
-size_t paged_attend_workspace_bytes(int64_t B, int d);
+size_t paged_attend_workspace_bytes(int d);
 Status launch_paged_attend(const PagedAttendRequest& q, cudaStream_t stream);
 bool paged_attend_tc_supported(const PagedAttendRequest& q);
 Status launch_paged_attend_tc(const PagedAttendRequest& q, cudaStream_t stream);

@@ -8,8 +8,7 @@
 // multiplied by 2^(m - m') (m in powers of two, beta log2(e) folded into the
 // scores).
 //
-// Here: the plan and the join (paged.cuh) that the tensor-core kernel of
-// paged_attend_tc.cu uses too, the dispatch, and the CUDA-core kernel, for
+// Here: the dispatch, and the CUDA-core kernel, for
 // float32 and for bf16 in shapes that the tensor cores' copies do not take
 // (d = 32, a page that is no multiple of 8 rows, strides that are no multiple
 // of 16 bytes).  It works in float32 throughout: one row tile is 64 rows, or 16
@@ -32,7 +31,6 @@ namespace {
 using namespace paged;
 
 constexpr int kM = 64, kN = 64, kThreads = 256;
-constexpr int kPlanThreads = 512;
 constexpr int kPad = 4;
 
 int paged_sm_count() {
@@ -259,25 +257,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     float* Qs = simt_sm;
     float* KVs = Qs + kM * (D + kPad);
     float* Ps = KVs + kN * (D + kPad);
-    const int64_t total = a.p.prefix[a.s.B];
-    const int active = active_blocks(total, a.G), c = blockIdx.x;
+    __shared__ ShareScratch scratch;
+    find_share<kN>(a.s, a.G, &scratch, &g_paged_attend_status);
+    __syncthreads();
     int4 join = make_int4(0, 0, 0, -1);
-    if (c < active) {
+    {
         Walk<kN> w;
-        w.start(a.s, a.p, block_start(total, active, c), block_start(total, active, c + 1));
+        w.start(a.s, scratch.share);
         Seg g;
         while (w.next(a.s, g)) {
             if (g.rows <= 16) simt_segment<E, D, 1>(a, g, Qs, KVs, Ps);
             else simt_segment<E, D, 4>(a, g, Qs, KVs, Ps);
-            if (g.t0 > 0 && g.t1 == g.nt) join = make_int4(g.b, g.h, g.t, block_of(total, active, g.unit_start));
+            if (g.t0 > 0 && g.t1 == g.nt) join = make_int4(g.b, g.h, g.t, scratch.share.line.block(g.first_end));
         }
     }
-    if (threadIdx.x == 0) a.p.joins[c] = join;
-}
-
-template <int N>
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(Shape s, Plan p) {
-    plan_block<N>(s, p, &g_paged_attend_status);
+    if (threadIdx.x == 0) a.p.joins[blockIdx.x] = join;
 }
 
 template <typename E, int D>
@@ -286,10 +280,10 @@ Status run_simt(const PagedAttendRequest& q, cudaStream_t st) {
     const int G = 2 * paged_sm_count();
     Carve cv(q.ws, q.ws_bytes);
     SimtArgs a{};
-    carve_plan(cv, &a.p, q.B, G, kM, D);
+    carve_plan(cv, &a.p, G, kM, D);
     if (!cv.fits()) return Status::fail(4, "paged_attend: workspace too small");
     a.s = Shape{q.table, q.table_stride, q.W, q.seq_lens, q.cu_new, q.T, q.pages, (int)q.B, q.Hkv, q.Hq / q.Hkv,
-                q.page_size, kM, q.causal};
+                q.page_size, kM, 16, 1, q.causal};
     a.Q = q.Q; a.K = q.K; a.V = q.V;
     a.q_t = q.q_t; a.q_h = q.q_h;
     a.k_p = q.k_p; a.k_h = q.k_h; a.k_r = q.k_r;
@@ -301,9 +295,8 @@ Status run_simt(const PagedAttendRequest& q, cudaStream_t st) {
     const int64_t all = q.q_t | q.q_h | q.k_p | q.k_h | q.k_r | q.v_p | q.v_h | q.v_r;
     const uintptr_t ptrs = reinterpret_cast<uintptr_t>(q.Q) | reinterpret_cast<uintptr_t>(q.K) | reinterpret_cast<uintptr_t>(q.V);
     a.wide = all % 4 == 0 && ptrs % (4 * sizeof(T)) == 0;
-    paged_plan_kernel<kN><<<1, kPlanThreads, 0, st>>>(a.s, a.p);
     const size_t smem = sizeof(float) * ((size_t)(kM + kN) * (D + kPad) + (size_t)kM * (kN + kPad));
-    cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<paged_simt_kernel<E, D>>((int)smem);
     if (e != cudaSuccess) return Status::cuda(e, "paged_attend: shared memory attribute");
     paged_simt_kernel<E, D><<<G, kThreads, smem, st>>>(a);
     e = cudaGetLastError();
@@ -313,11 +306,11 @@ Status run_simt(const PagedAttendRequest& q, cudaStream_t st) {
 
 }  // namespace
 
-size_t paged_attend_workspace_bytes(int64_t B, int d) {
+size_t paged_attend_workspace_bytes(int d) {
     const int sms = paged_sm_count();
     Plan p;
     Carve a(nullptr, 0), b(nullptr, 0);
-    const size_t simt = carve_plan(a, &p, B, 2 * sms, kM, d), tc = carve_plan(b, &p, B, sms, kPagedTcRows, d);
+    const size_t simt = carve_plan(a, &p, 2 * sms, kM, d), tc = carve_plan(b, &p, sms, kPagedTcRows, d);
     return std::max(simt, tc) + 256;
 }
 

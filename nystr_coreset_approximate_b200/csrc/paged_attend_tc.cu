@@ -62,7 +62,6 @@ using namespace paged;
 
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kThreads = 512;
-constexpr int kPlanThreads = 512;
 // registers per thread after the split: 96 + 2 * 168 + 80 = 512 per lane of a
 // sub-partition, the 4 * 128 it was launched with
 constexpr int kRegsLow = 96, kRegsSoftmax = 168, kRegsEpilogue = 80;
@@ -177,24 +176,24 @@ struct Pages {
         L = g.L;
         t1 = g.t1;
     }
-    // the copy of a page past the pool fills zeros
+    // the table's entry for this lane's page of a tile (not looked at yet: it may be on its way)
     __device__ __forceinline__ int id(const TcArgs& a, int kt, int lane) const {
         const int j = kt * kKeys + lane * a.box;
-        int page = (int)a.s.pages;
-        if (lane * a.box < kKeys && j < L) {
-            const int v = __ldg(row + (unsigned)j / (unsigned)a.s.page_size);
-            if (v >= 0 && v < a.s.pages) page = v;
-            else atomicMax(&g_paged_tc_status, 1);
-        }
-        return page;
+        return kt < t1 && lane * a.box < kKeys && j < L ? __ldg(row + (unsigned)j / (unsigned)a.s.page_size) : 0;
     }
-    // bring the ids of a later tile into L1: a lookup from L2 or HBM takes as long as a tile's copy
+    // what the copy takes: past the pool it fills zeros
+    __device__ __forceinline__ int check(const TcArgs& a, int id, int kt, int lane) const {
+        const int j = kt * kKeys + lane * a.box;
+        if (lane * a.box >= kKeys || j >= L) return (int)a.s.pages;
+        if (id >= 0 && id < a.s.pages) return id;
+        atomicMax(&g_paged_tc_status, 1);
+        return (int)a.s.pages;
+    }
+    // bring the entries of a later tile into L2: a read from HBM takes as long as a tile's copy
     __device__ __forceinline__ void touch(const TcArgs& a, int kt, int lane) const {
         const int j = kt * kKeys + lane * a.box;
-        if (kt < t1 && lane * a.box < kKeys && j < L) {
-            int dummy;
-            asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(dummy) : "l"(row + (unsigned)j / (unsigned)a.s.page_size));
-        }
+        if (kt < t1 && lane * a.box < kKeys && j < L)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row + (unsigned)j / (unsigned)a.s.page_size));
     }
 };
 
@@ -207,18 +206,17 @@ __device__ __forceinline__ void copy_tile(const TcArgs& a, const CUtensorMap* tm
     const int row = boxes > 1 ? 0 : (int)((unsigned)(kt * kKeys) % (unsigned)a.s.page_size);
     if (elect_one()) mbar_expect_tx(full, C::t_bytes);
     __syncwarp();
-    for (int p0 = 0; p0 < boxes; p0 += 8) {
-        int page[8];
-#pragma unroll
-        for (int p = 0; p < 8; ++p) page[p] = __shfl_sync(0xffffffffu, id, p0 + p);
+#pragma unroll 1
+    for (int p = 0; p < boxes; p += 2) {  // two pages at a time
+        const int p0 = __shfl_sync(0xffffffffu, id, p), p1 = __shfl_sync(0xffffffffu, id, p + 1);
         if (elect_one()) {
+            const unsigned at = dst + (unsigned)(p * a.box) * 128u;
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                if (p0 + p >= boxes) break;
+            for (int kb = 0; kb < C::KB; ++kb) tma_load_4d(at + kb * C::blk, tm, kb * 64, row, h, p0, full);
+            if (p + 1 < boxes)
 #pragma unroll
                 for (int kb = 0; kb < C::KB; ++kb)
-                    tma_load_4d(dst + (unsigned)((p0 + p) * a.box) * 128u + kb * C::blk, tm, kb * 64, row, h, page[p], full);
-            }
+                    tma_load_4d(at + (unsigned)a.box * 128u + kb * C::blk, tm, kb * 64, row, h, p1, full);
         }
         __syncwarp();
     }
@@ -228,7 +226,7 @@ __device__ __forceinline__ void copy_tile(const TcArgs& a, const CUtensorMap* tm
 // and its V tiles.
 template <int D, bool V>
 __device__ __forceinline__ void role_copy(const Ctx<D>& x, const TcArgs& a, const CUtensorMap* tmQ, const CUtensorMap* tm,
-                                          int lane, int64_t lo, int64_t hi, int64_t total, int active) {
+                                          int lane, const Share& share) {
     using C = Cfg<D>;
     constexpr int N = V ? C::NV : C::NK;
     auto* bars = x.bars;
@@ -245,60 +243,74 @@ __device__ __forceinline__ void role_copy(const Ctx<D>& x, const TcArgs& a, cons
     Walk<kKeys> w;
     unsigned pushed = 0;
     bool more = !V;
-    if (!V) w.start(a.s, a.p, lo, hi);
-    for (unsigned s = 0; ok; ++s) {
-        while (more && pushed < s + kLead && ok) {
-            if (pushed >= kItems) ok = x.wait(&bars->item_empty[pushed % kItems], pushed / kItems - 1);
-            if (!ok) break;
-            Seg g;
-            more = w.next(a.s, g);
-            if (lane == 0) {
-                Item* it = x.item(pushed);
-                if (more) {
-                    const bool ends = g.t0 > 0 && g.t1 == g.nt;  // the last piece of a cut unit
-                    *it = Item{g.b, g.h, g.t, g.n, g.L, g.row0, g.rows, g.t0, g.t1, g.nt, a.s.first_row(g.b),
-                               ends ? block_of(total, active, g.unit_start) : -1};
-                } else {
-                    it->t0 = it->t1 = 0;
-                }
-                mbar_arrive(&bars->item_full[pushed % kItems]);
+    if (!V) w.start(a.s, share);
+    auto push = [&]() {  // one more segment into the ring
+        if (pushed >= kItems && !x.wait(&bars->item_empty[pushed % kItems], pushed / kItems - 1)) return false;
+        Seg g;
+        more = w.next(a.s, g);
+        if (lane == 0) {
+            Item* it = x.item(pushed);
+            if (more) {
+                const bool ends = g.t0 > 0 && g.t1 == g.nt;  // the last piece of a cut unit
+                *it = Item{g.b, g.h, g.t, g.n, g.L, g.row0, g.rows, g.t0, g.t1, g.nt, a.s.first_row(g.b),
+                           ends ? share.line.block(g.first_end) : -1};
+            } else {
+                it->t0 = it->t1 = 0;
             }
-            __syncwarp();
-            ++pushed;
+            mbar_arrive(&bars->item_full[pushed % kItems]);
         }
+        __syncwarp();
+        ++pushed;
+        return true;
+    };
+    Item g;
+    g.t1 = 0;
+    Pages<D> pages;
+    int kt = 0, next = 0;
+    for (unsigned s = 0;;) {
+#pragma unroll 1
+        for (int e = 0; e < 2 && more && pushed < s + kLead && ok; ++e) ok = push();
         if (!ok) break;
-        ok = x.item_wait(s);
-        if (!ok) break;
-        const Item g = *x.item(s);
-        x.item_done(s, lane);
-        if (g.t1 == g.t0) break;
-        Pages<D> pages;
-        pages.of(a, g);
-        for (int e = 0; e < kAhead; ++e) pages.touch(a, g.t0 + e, lane);
-        if (V) {
-            const int tiles = g.rows > a.R ? 2 : 1;
-            for (int e = 0; e < tiles && ok; ++e, ++qn) {
-                const unsigned qb = qn & 1u;
-                if (qn >= 2) ok = x.wait(&bars->q_free[qb], qn / 2 - 1);
-                if (!ok) break;
-                if (elect_one()) {
-                    mbar_expect_tx(&bars->q_full[qb], (unsigned)a.R * 128u * C::KB);
-                    const int token = g.first + (g.row0 + e * a.R) / a.s.g;
+        if (kt == g.t1) {  // the next segment
+            ok = x.item_wait(s);
+            if (!ok) break;
+            g = *x.item(s);
+            x.item_done(s, lane);
+            if (g.t1 == g.t0) break;
+            ++s;
+            kt = g.t0;
+            pages.of(a, g);
+            for (int e = 0; e < kAhead; ++e) pages.touch(a, kt + e, lane);
+            if (V) {
+                const int tiles = g.rows > a.R ? 2 : 1;
+#pragma unroll 1
+                for (int e = 0; e < tiles && ok; ++e, ++qn) {
+                    const unsigned qb = qn & 1u;
+                    if (qn >= 2) ok = x.wait(&bars->q_free[qb], qn / 2 - 1);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        mbar_expect_tx(&bars->q_full[qb], (unsigned)a.R * 128u * C::KB);
+                        const int token = g.first + (g.row0 + e * a.R) / a.s.g;
 #pragma unroll
-                    for (int kb = 0; kb < C::KB; ++kb)
-                        tma_load_4d(x.sbase + C::off_q + qb * C::q_bytes + kb * (kRows * 128), tmQ, kb * 64, 0, g.h, token,
-                                    &bars->q_full[qb]);
+                        for (int kb = 0; kb < C::KB; ++kb)
+                            tma_load_4d(x.sbase + C::off_q + qb * C::q_bytes + kb * (kRows * 128), tmQ, kb * 64, 0, g.h, token,
+                                        &bars->q_full[qb]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
             }
+            next = pages.id(a, kt, lane);
         }
-        for (int kt = g.t0; kt < g.t1 && ok; ++kt, r.next(), ++n) {
-            pages.touch(a, kt + kAhead, lane);
-            const int id = pages.id(a, kt, lane);
-            if (n >= N) ok = x.wait(&empty[r.s], r.ph ^ 1u);
-            if (!ok) break;
-            copy_tile<D>(a, tm, base + (unsigned)r.s * C::t_bytes, kt, g.h, id, &full[r.s]);
-        }
+        pages.touch(a, kt + kAhead, lane);
+        const int id = pages.check(a, next, kt, lane);
+        next = pages.id(a, kt + 1, lane);
+        if (n >= N) ok = x.wait(&empty[r.s], r.ph ^ 1u);
+        if (!ok) break;
+        copy_tile<D>(a, tm, base + (unsigned)r.s * C::t_bytes, kt, g.h, id, &full[r.s]);
+        r.next();
+        ++n;
+        ++kt;
     }
     if (!ok && lane == 0) x.give_up();
     __syncwarp();
@@ -407,6 +419,7 @@ __device__ __forceinline__ void role_mma(const Ctx<D>& x, const TcArgs& a) {
         unsigned par0 = pn / 2, par1 = (pn + 1) / 2;
         unsigned go = sn - 1;
         const int m = (k.n - 2 - k.i) / 2;
+#pragma unroll 1
         for (int e = 0; e < m; ++e) {
             const uint32_t kd = k_lo + (uint32_t)kr.s * (C::t_bytes >> 4), vd = v_lo + (uint32_t)vr.s * (C::t_bytes >> 4);
             if (!x.wait_one(&bars->k_full[kr.s], kr.ph) || !x.wait_one(&bars->s_go, go)) return false;
@@ -439,13 +452,14 @@ __device__ __forceinline__ void role_mma(const Ctx<D>& x, const TcArgs& a) {
         pn += 2 * m;
         return true;
     };
-    for (int e = 0; e < 2 && ok && k.n > 0; ++e) ok = scores();
-    while (ok && v.n > 0) {
+#pragma unroll 1
+    for (int step = 0; ok && v.n > 0; ++step) {
         if (v.two && v.i == 2 && k.s == v.s && k.n - k.i > 2) {
             ok = pairs();
             if (!ok) break;
         }
         if (k.n > 0) ok = scores();
+        if (step < 2) continue;
         const unsigned t = pn & 1u;
         if (ok && v.opens()) {
             vs = vr.s;
@@ -527,6 +541,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<D>& x, const TcArgs& a, u
         ok = x.item_wait(s);
         if (!ok) break;
         int lim, step, ops, rows;
+        bool mine;
         {
             const Item g = *x.item(s);
             x.item_done(s, lane);
@@ -537,7 +552,9 @@ __device__ __forceinline__ void role_softmax(const Ctx<D>& x, const TcArgs& a, u
             ops = (n - i0 + 1) >> 1;
             const int tile = two ? i0 : 0, r = tile * a.R + row;
             rows = min(g.rows - tile * a.R, a.R);
-            const int end = row < rows ? (a.s.causal ? g.L - g.n + (g.row0 + r) / a.s.g + 1 : g.L) : 0;
+            // rows past the unit's are formed like the others and not used
+            const int end = a.s.causal && row < rows ? g.L - g.n + (g.row0 + r) / a.s.g + 1 : g.L;
+            mine = row < rows;
             lim = end - (g.t0 + (two ? 0 : i0)) * kKeys;  // keys of the tile that the row sees
             step = two ? kKeys : 2 * kKeys;
         }
@@ -567,18 +584,51 @@ __device__ __forceinline__ void role_softmax(const Ctx<D>& x, const TcArgs& a, u
             if (active) {
                 if (__any_sync(0xffffffffu, lim < kKeys)) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 4; ++j) {
+                        const int left = lim - 32 * j;
+                        const uint32_t seen = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (32 * j + e >= lim) v[j][e] = 0xff800000u;
+                            if (!(seen >> e & 1u)) v[j][e] = 0xff800000u;
+                    }
                 }
                 float sum;
-                auto exps = [&]() {  // P, and its sum
+                // Once with the maximum so far, and once more where it has to be raised; the first
+                // tile begins with its maximum.  (One copy of this code: the roles' loops together
+                // have to stay in the instruction cache.)
+                bool raise = c == 0;
+#pragma unroll 1
+                for (;;) {
+                    if (raise) {
+                        float best[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            best[j] = __uint_as_float(v[j][0]);
+#pragma unroll
+                            for (int e = 1; e < 32; ++e) best[j] = fmaxf(best[j], __uint_as_float(v[j][e]));
+                        }
+                        const float mt = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * a.scale;
+                        const float mn = fmaxf(m, mt);
+                        if (c > 0) {
+                            const float f = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
+                            l *= f;
+#pragma unroll 1
+                            for (int cc = 0; cc < D; cc += 16) {
+                                float acc[16];
+                                uint32_t w[16];
+                                tmem_ld16(tO + cc, acc);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(acc[e] * f);
+                                tmem_st16(tO + cc, w);
+                            }
+                        }
+                        m = mn;
+                    }
                     const float base = m == -INFINITY ? 0.f : m;
                     const float2 nb = make_float2(-base, -base);
                     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 4; ++j) {  // P, and its sum
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
@@ -591,37 +641,9 @@ __device__ __forceinline__ void role_softmax(const Ctx<D>& x, const TcArgs& a, u
                         tmem_st16(tP + 16 * j, pk);
                     }
                     sum = (part[0].x + part[0].y) + (part[1].x + part[1].y);
-                };
-                bool redo = c == 0;
-                if (c > 0) {
-                    exps();
-                    redo = __any_sync(0xffffffffu, sum > kRaise || (m == -INFINITY && lim > 0));
-                }
-                if (redo) {
-                    float best[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        best[j] = __uint_as_float(v[j][0]);
-#pragma unroll
-                        for (int e = 1; e < 32; ++e) best[j] = fmaxf(best[j], __uint_as_float(v[j][e]));
-                    }
-                    const float mt = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * a.scale;
-                    const float mn = fmaxf(m, mt);
-                    if (c > 0) {
-                        const float f = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
-                        l *= f;
-#pragma unroll 1
-                        for (int cc = 0; cc < D; cc += 16) {
-                            float acc[16];
-                            uint32_t w[16];
-                            tmem_ld16(tO + cc, acc);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(acc[e] * f);
-                            tmem_st16(tO + cc, w);
-                        }
-                    }
-                    m = mn;
-                    exps();
+                    if (raise) break;
+                    raise = __any_sync(0xffffffffu, mine && (sum > kRaise || (m == -INFINITY && lim > 0)));
+                    if (!raise) break;
                 }
                 l += sum;
                 tmem_wait_st();
@@ -731,12 +753,10 @@ __device__ __forceinline__ void role_epilogue(const Ctx<D>& x, const TcArgs& a, 
         x.item_done(s, lane);
         if (g.t1 == g.t0) break;
         const int s0 = (int)(k0 & 1u), n = g.t1 - g.t0;
-        if (g.rows > a.R) {
-            ok = put_tile<D>(x, a, g, 0, s0, false, on, quad, lane) && put_tile<D>(x, a, g, 1, s0 ^ 1, false, on, quad, lane);
-        } else {
-            ok = put_tile<D>(x, a, g, 0, s0, n > 1, on, quad, lane);
-            k0 += n;
-        }
+        const int tiles = g.rows > a.R ? 2 : 1;
+#pragma unroll 1
+        for (int e = 0; e < tiles && ok; ++e) ok = put_tile<D>(x, a, g, e, s0 ^ e, tiles == 1 && n > 1, on, quad, lane);
+        if (tiles == 1) k0 += n;
         if (g.join >= 0) join = make_int4(g.b, g.h, g.t, g.join);
     }
     if (!ok && lane == 0) x.give_up();
@@ -756,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     x.bars = reinterpret_cast<Bars<C::NK, C::NV>*>(sm + C::off_bar);
     x.abort_flag = &x.bars->abort;
     auto* bars = x.bars;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's prologue
     if (tid == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars->q_full[t], 1);
@@ -800,22 +820,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     x.tmem = bars->tmem_base;
     const bool go = *x.abort_flag == 0;
-    // the plan has been made
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t total = a.p.prefix[a.s.B];
-    const int active = active_blocks(total, a.G), c = blockIdx.x;
-    const int64_t lo = c < active ? block_start(total, active, c) : 0, hi = c < active ? block_start(total, active, c + 1) : 0;
+    ShareScratch* scratch = reinterpret_cast<ShareScratch*>(sm + C::off_ml);
+    find_share<kKeys>(a.s, a.G, scratch, &g_paged_tc_status);
+    __syncthreads();
+    const Share share = scratch->share;
+    __syncthreads();  // the softmax groups write there
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (go) {
-            if (warp == 0) role_copy<D, false>(x, a, &tmQ, &tmK, lane, lo, hi, total, active);
+            if (warp == 0) role_copy<D, false>(x, a, &tmQ, &tmK, lane, share);
             else if (warp == 1) {
                 if (elect_one()) role_mma<D>(x, a);
                 __syncwarp();
             }
             else if (warp == 2) role_tail<D>(x, lane);
-            else role_copy<D, true>(x, a, &tmQ, &tmV, lane, lo, hi, total, active);
+            else role_copy<D, true>(x, a, &tmQ, &tmV, lane, share);
         }
         __syncwarp();
     } else if (warp < 12) {
@@ -824,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsEpilogue));
         if (go) role_epilogue<D>(x, a, warp & 3, lane);
-        else if (warp == 12 && lane == 0) a.p.joins[c] = make_int4(0, 0, 0, -1);
+        else if (warp == 12 && lane == 0) a.p.joins[blockIdx.x] = make_int4(0, 0, 0, -1);
     }
 
     tc_fence_before();
@@ -834,11 +854,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(x.tmem), "r"(C::tmem_cols)
                      : "memory");
     }
-}
-
-__global__ void __launch_bounds__(kPlanThreads) paged_tc_plan_kernel(Shape s, Plan p) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    plan_block<kKeys>(s, p, &g_paged_tc_status);
 }
 
 int sm_count() {
@@ -856,10 +871,10 @@ Status run_tc(const PagedAttendRequest& q, cudaStream_t st) {
     const int G = sm_count(), g = q.Hq / q.Hkv, R = kRows / g * g;
     Carve cv(q.ws, q.ws_bytes);
     TcArgs a{};
-    carve_plan(cv, &a.p, q.B, G, kPagedTcRows, D);
+    carve_plan(cv, &a.p, G, kPagedTcRows, D);
     if (!cv.fits()) return Status::fail(4, "paged_attend: workspace too small");
     a.s = Shape{q.table, q.table_stride, q.W, q.seq_lens, q.cu_new, q.T, q.pages, (int)q.B, q.Hkv, g,
-                q.page_size, 2 * R, q.causal};
+                q.page_size, 2 * R, R, 1, q.causal};
     a.O = static_cast<__nv_bfloat16*>(q.O);
     a.o_t = q.o_t;
     a.o_h = q.o_h;
@@ -880,24 +895,10 @@ Status run_tc(const PagedAttendRequest& q, cudaStream_t st) {
         make_tmap_4d(&tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q.V, {Du, ps, H, P},
                      {(uint64_t)q.v_r * 2, (uint64_t)q.v_h * 2, (uint64_t)q.v_p * 2}, {64u, box, 1u, 1u});
     if (!ok) return Status::fail(3, "paged_attend: tensor map encoding failed");
-    cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::total);
+    cudaError_t e = allow_smem<paged_tc_kernel<D>>((int)C::total);
     if (e != cudaSuccess) return Status::cuda(e, "paged_attend: shared memory attribute");
-    paged_tc_plan_kernel<<<1, kPlanThreads, 0, st>>>(a.s, a.p);
+    paged_tc_kernel<D><<<G, kThreads, C::total, st>>>(tmQ, tmK, tmV, a);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return Status::cuda(e, "paged_attend: plan launch");
-    // a programmatic dependent of the plan: its prologue overlaps it
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)G);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::total;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, paged_tc_kernel<D>, tmQ, tmK, tmV, a);
-    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return Status::cuda(e, "paged_attend launch");
     return launch_paged_join(PagedJoin{a.s, a.p, q.O, q.o_t, q.o_h, q.lse, G}, q.dtype, D, kPagedTcRows, st);
 }
