@@ -7,8 +7,9 @@
 // in float32, rounded once.  Of the unit that ends in block c and begins in c0,
 // block c0 holds the first piece (its slot 1: it begins the unit), blocks c0 +
 // 1 .. c the others (slot 0).  At most one unit ends so in each block.  A warp
-// takes one row; four blocks share a unit's rows.  Bounded by the reads of the
-// pieces, which are in L2.
+// takes a row or two.  Bounded by the latency of its reads, one after the other
+// (the unit, its rows, the pieces' sums, the pieces, which are in L2): with 16
+// rows to a warp it took 20 us for 148 units of 256 rows.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.cuh"
@@ -18,7 +19,7 @@ namespace wildcat {
 namespace {
 
 using namespace paged;
-constexpr int kJoinThreads = 256, kJoinSplit = 4;
+constexpr int kJoinThreads = 256, kJoinRows = 2;  // rows of a warp
 
 template <typename E, int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedJoin a, int M) {
@@ -34,11 +35,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedJoin a, i
     const int rows = (int)min((int64_t)a.s.M, (int64_t)n * a.s.g - row0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int W = D / 32;
-    for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < rows; r += kJoinSplit * (kJoinThreads / 32)) {
+    for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < rows; r += gridDim.y * (kJoinThreads / 32)) {
         float m = -INFINITY;
+        float2 mine = make_float2(-INFINITY, 0.f);  // of piece `lane`
         for (int k = lane; k < pieces; k += 32) {
-            const int64_t at = ((int64_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * M + r;
-            m = fmaxf(m, a.p.ml[at].x);
+            const float2 ml = a.p.ml[((int64_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * M + r];
+            if (k < 32) mine = ml;
+            m = fmaxf(m, ml.x);
         }
         m = warp_max(m);
         const float base = m == -INFINITY ? 0.f : m;
@@ -48,7 +51,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedJoin a, i
 #pragma unroll 4
         for (int k = 0; k < pieces; ++k) {
             const int64_t at = ((int64_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * M + r;
-            const float2 ml = a.p.ml[at];
+            float2 ml = make_float2(__shfl_sync(0xffffffffu, mine.x, k & 31), __shfl_sync(0xffffffffu, mine.y, k & 31));
+            if (k >= 32) ml = a.p.ml[at];
             const float f = exp2f(ml.x - base);
             l = fmaf(f, ml.y, l);
             const float* src = a.p.part + at * D + lane * W;
@@ -82,7 +86,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedJoin a, i
 template <typename E, int D>
 Status run_join(const PagedJoin& a, int M, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.G, kJoinSplit);
+    cfg.gridDim = dim3((unsigned)a.G, (unsigned)(M / (kJoinRows * kJoinThreads / 32)));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
