@@ -25,6 +25,7 @@ that are not compressed yet, or not at all; one step of a serving program:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional
@@ -774,6 +775,11 @@ def paged_write(k, v, slots, k_pool, v_pool, *, q=None, positions=None, inv_freq
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _attend_workspace(device: int, B: int, d: int) -> int:
+    return int(lib().wildcat_paged_attend_workspace_size(B, d))
+
+
 def paged_attend(q, k_pool, v_pool, block_table, seq_lens, cu_new, beta: float, *, causal: bool = True, lse=None,
                  out=None, stream=None):
     """Exact attention of new tokens over the paged cache.  q [T, Hq, d]
@@ -817,7 +823,7 @@ def paged_attend(q, k_pool, v_pool, block_table, seq_lens, cu_new, beta: float, 
         op, (ot, oh, _) = _rows(out, "out", 3, dev, dtype)
     L = lib()
     W = block_table.shape[1]
-    nbytes = L.wildcat_paged_attend_workspace_size(B, d)
+    nbytes = _attend_workspace(dev, B, d)
     ws = _empty(nbytes, torch.uint8, q.device, stream)
     _check(L.wildcat_paged_attend(qp, qt, qh, kpp, _Strides3(*ks[:3]), vpp, _Strides3(*vs[:3]), pages, page_size, code, T, Hq,
                                   Hkv, d, table, rows[0] if B > 1 else max(W, 1), W, lens, cu, B, float(beta), 1 if causal else 0,

@@ -71,6 +71,7 @@ constexpr int kItems = 8;  // segments in the ring
 constexpr int kLead = 5;   // segments that warp 2 hands out ahead of its own
 constexpr float kRaise = 65536.f;  // a row's sum of one tile above which its maximum is raised
 constexpr int kAhead = 3;  // key tiles between the first touch of their page ids and their use
+constexpr int kPagesOfTile = kKeys / 8;
 
 // One segment: key tiles [t0, t1) of a unit; t1 == t0 ends the ring.
 struct Item {
@@ -92,7 +93,7 @@ template <int D>
 struct Cfg {
     static constexpr int KB = D / 64;                   // 128-byte blocks of a row
     static constexpr int NK = D == 128 ? 3 : 6;         // stages of K tiles: two operations more are on their way
-    static constexpr int NV = D == 128 ? 2 : 6;         // stages of V tiles
+    static constexpr int NV = D == 128 ? 2 : 5;         // stages of V tiles
     static constexpr uint32_t q_bytes = kRows * D * 2;  // one row tile
     static constexpr uint32_t t_bytes = kKeys * D * 2;  // one tile of K or V
     static constexpr uint32_t blk = kKeys * 128;        // one 128-byte block of a tile
@@ -101,7 +102,8 @@ struct Cfg {
     static constexpr uint32_t off_v = off_k + NK * t_bytes;
     static constexpr uint32_t off_ml = off_v + NV * t_bytes;  // (m, l) of each slot's rows
     static constexpr uint32_t off_items = off_ml + 2 * kRows * 8;
-    static constexpr uint32_t off_bar = off_items + kItems * (uint32_t)sizeof(Item);
+    static constexpr uint32_t off_ids = off_items + kItems * (uint32_t)sizeof(Item);  // a tile's pages: K, V
+    static constexpr uint32_t off_bar = off_ids + 2 * kPagesOfTile * 4;
     static constexpr uint32_t total = off_bar + (uint32_t)sizeof(Bars<NK, NV>);
     static constexpr unsigned tmem_cols = 512;
     static constexpr unsigned col_O = 0;      // O of slot t at t * D
@@ -165,60 +167,76 @@ struct Ring {
     }
 };
 
-// The page ids of a segment's key tiles: lane p has page p of a tile.
-template <int D>
+// The page ids of a segment's key tiles, one tile after the other: lane p has page p
+// of a tile.
 struct Pages {
     const int32_t* row;  // the request's row of the table
-    int L, t1;
+    int count;           // its pages
+    int ix, sub;         // the entry of the tile read next, and which tile of its page that is
+    int boxes, tiles;    // pages of a tile; tiles of a page
+    int last;            // the entry read last, -1 for none
 
-    __device__ __forceinline__ void of(const TcArgs& a, const Item& g) {
+    __device__ __forceinline__ void of(const TcArgs& a, const Item& g, int lane) {
         row = a.s.table + (int64_t)g.b * a.s.table_stride;
-        L = g.L;
-        t1 = g.t1;
+        count = ((unsigned)g.L + (unsigned)a.s.page_size - 1u) / (unsigned)a.s.page_size;
+        boxes = kKeys / a.box;
+        tiles = (unsigned)a.s.page_size / (unsigned)a.box;
+        ix = boxes > 1 ? g.t0 * boxes + lane : (unsigned)g.t0 / (unsigned)tiles;
+        sub = boxes > 1 ? 0 : g.t0 - ix * tiles;
+        if (lane >= boxes) count = 0;
+        if (lane == 0)
+            for (int e = 0; e < kAhead; ++e) touch(e);
     }
-    // the table's entry for this lane's page of a tile (not looked at yet: it may be on its way)
-    __device__ __forceinline__ int id(const TcArgs& a, int kt, int lane) const {
-        const int j = kt * kKeys + lane * a.box;
-        return kt < t1 && lane * a.box < kKeys && j < L ? __ldg(row + (unsigned)j / (unsigned)a.s.page_size) : 0;
+    // the next tile's entry (not looked at yet: it may be on its way)
+    __device__ __forceinline__ int read() {
+        const bool there = ix < count;
+        const int id = there ? __ldg(row + ix) : 0;
+        last = there ? ix : -1;
+        if (boxes > 1) {
+            ix += boxes;
+        } else if (++sub == tiles) {
+            sub = 0;
+            ++ix;
+        }
+        return id;
     }
-    // what the copy takes: past the pool it fills zeros
-    __device__ __forceinline__ int check(const TcArgs& a, int id, int kt, int lane) const {
-        const int j = kt * kKeys + lane * a.box;
-        if (lane * a.box >= kKeys || j >= L) return (int)a.s.pages;
+    // what the copy takes for an entry that was read at `at`: past the pool it fills zeros
+    __device__ __forceinline__ int check(const TcArgs& a, int id, int at) const {
+        if (at < 0) return (int)a.s.pages;
         if (id >= 0 && id < a.s.pages) return id;
         atomicMax(&g_paged_tc_status, 1);
         return (int)a.s.pages;
     }
     // bring the entries of a later tile into L2: a read from HBM takes as long as a tile's copy
-    __device__ __forceinline__ void touch(const TcArgs& a, int kt, int lane) const {
-        const int j = kt * kKeys + lane * a.box;
-        if (kt < t1 && lane * a.box < kKeys && j < L)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(row + (unsigned)j / (unsigned)a.s.page_size));
+    __device__ __forceinline__ void touch(int ahead) const {
+        const int at = ix + ahead * boxes;
+        if (at < count) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
     }
 };
 
-// One tile of K or V, page by page, by one lane.
+// One tile of K or V, page by page, by one lane; `ids` holds the pages in shared memory.
 template <int D>
-__device__ __forceinline__ void copy_tile(const TcArgs& a, const CUtensorMap* tm, unsigned dst, int kt, int h, int id,
-                                          uint64_t* full) {
+__device__ __forceinline__ void copy_pages(const CUtensorMap* tm, unsigned dst, unsigned page_bytes, int row, int h, int boxes,
+                                           const int* ids, uint64_t* full) {
     using C = Cfg<D>;
-    const int boxes = kKeys / a.box;
-    const int row = boxes > 1 ? 0 : (int)((unsigned)(kt * kKeys) % (unsigned)a.s.page_size);
-    if (elect_one()) mbar_expect_tx(full, C::t_bytes);
-    __syncwarp();
+    mbar_expect_tx(full, C::t_bytes);
+    if (boxes >= 4) {
 #pragma unroll 1
-    for (int p = 0; p < boxes; p += 2) {  // two pages at a time
-        const int p0 = __shfl_sync(0xffffffffu, id, p), p1 = __shfl_sync(0xffffffffu, id, p + 1);
-        if (elect_one()) {
-            const unsigned at = dst + (unsigned)(p * a.box) * 128u;
+        for (int p = 0; p < boxes; p += 4, dst += 4 * page_bytes) {
+            const int4 id = *reinterpret_cast<const int4*>(ids + p);
 #pragma unroll
-            for (int kb = 0; kb < C::KB; ++kb) tma_load_4d(at + kb * C::blk, tm, kb * 64, row, h, p0, full);
-            if (p + 1 < boxes)
-#pragma unroll
-                for (int kb = 0; kb < C::KB; ++kb)
-                    tma_load_4d(at + (unsigned)a.box * 128u + kb * C::blk, tm, kb * 64, row, h, p1, full);
+            for (int kb = 0; kb < C::KB; ++kb) {
+                tma_load_4d(dst + kb * C::blk, tm, kb * 64, row, h, id.x, full);
+                tma_load_4d(dst + page_bytes + kb * C::blk, tm, kb * 64, row, h, id.y, full);
+                tma_load_4d(dst + 2 * page_bytes + kb * C::blk, tm, kb * 64, row, h, id.z, full);
+                tma_load_4d(dst + 3 * page_bytes + kb * C::blk, tm, kb * 64, row, h, id.w, full);
+            }
         }
-        __syncwarp();
+    } else {
+#pragma unroll 1
+        for (int p = 0; p < boxes; ++p, dst += page_bytes)
+#pragma unroll
+            for (int kb = 0; kb < C::KB; ++kb) tma_load_4d(dst + kb * C::blk, tm, kb * 64, row, h, ids[p], full);
     }
 }
 
@@ -265,8 +283,9 @@ __device__ __forceinline__ void role_copy(const Ctx<D>& x, const TcArgs& a, cons
     };
     Item g;
     g.t1 = 0;
-    Pages<D> pages;
+    Pages pages;
     int kt = 0, next = 0;
+    int* ids = reinterpret_cast<int*>(x.sm + C::off_ids) + (V ? kPagesOfTile : 0);
     for (unsigned s = 0;;) {
 #pragma unroll 1
         for (int e = 0; e < 2 && more && pushed < s + kLead && ok; ++e) ok = push();
@@ -279,8 +298,7 @@ __device__ __forceinline__ void role_copy(const Ctx<D>& x, const TcArgs& a, cons
             if (g.t1 == g.t0) break;
             ++s;
             kt = g.t0;
-            pages.of(a, g);
-            for (int e = 0; e < kAhead; ++e) pages.touch(a, kt + e, lane);
+            pages.of(a, g, lane);
             if (V) {
                 const int tiles = g.rows > a.R ? 2 : 1;
 #pragma unroll 1
@@ -300,14 +318,19 @@ __device__ __forceinline__ void role_copy(const Ctx<D>& x, const TcArgs& a, cons
                 }
                 if (!ok) break;
             }
-            next = pages.id(a, kt, lane);
+            next = pages.read();
         }
-        pages.touch(a, kt + kAhead, lane);
-        const int id = pages.check(a, next, kt, lane);
-        next = pages.id(a, kt + 1, lane);
+        if (lane == 0) pages.touch(kAhead);
+        const int id = pages.check(a, next, pages.last);
+        const int row = pages.boxes > 1 ? 0 : (kt - (pages.ix - (pages.sub == 0 ? 1 : 0)) * pages.tiles) * kKeys;
+        if (lane < kPagesOfTile) ids[lane] = id;
+        next = pages.read();
         if (n >= N) ok = x.wait(&empty[r.s], r.ph ^ 1u);
         if (!ok) break;
-        copy_tile<D>(a, tm, base + (unsigned)r.s * C::t_bytes, kt, g.h, id, &full[r.s]);
+        __syncwarp();
+        if (elect_one())
+            copy_pages<D>(tm, base + (unsigned)r.s * C::t_bytes, (unsigned)a.box * 128u, row, g.h, pages.boxes, ids, &full[r.s]);
+        __syncwarp();
         r.next();
         ++n;
         ++kt;
