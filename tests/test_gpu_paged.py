@@ -445,3 +445,70 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+# ------------------------------------------------------------ more that can go wrong
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,page", [(130, 1, 16), (33, 1, 128), (128, 1, 8), (48, 2, 64)], ids=str)
+def test_attend_wide_groups(dtype, Hq, Hkv, page):
+    """More query heads to a key head than a tile has rows, and numbers that do not divide it."""
+    _attend_check(pc.paged_inputs(Hq, [150, 300, 2], [3, 9, 1], Hq, Hkv, 64, page, dtype, extra_rows=1), 0.125)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_attend_more_requests_than_threads(dtype):
+    """Requests without new tokens among them, and some without anything."""
+    rng = random.Random(5)
+    lens = [rng.choice([0, 1, 15, 16, 17, 60]) for _ in range(1300)]
+    new = [rng.choice([0, 0, 1, 2]) for _ in range(1300)]
+    _attend_check(pc.paged_inputs(13, lens, new, 2, 1, 64, 16, dtype), 0.125)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_long_chunks_beside_short_ones(dtype, causal):
+    """Many row tiles to a request, most of whose rows see nothing (causal: 900 new tokens of 260)."""
+    _attend_check(pc.paged_inputs(14, [260, 700, 33], [900, 700, 1], 5, 1, 64, 32, dtype), 0.125, causal)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 100])
+def test_attend_scores_that_leap(d, new):
+    """A key every few tiles scores far above all before it, so that exponentials with the maximum of the tiles before
+    overflow; in between they vanish."""
+    c = pc.paged_inputs(15, [1500], [new], 4, 2, d, 16, BF)
+    for x in (140, 141, 400, 900, 1290, 1399):
+        c["k_pool"][c["table"][0][x // 16], :, x % 16] *= 1 + x / 50
+    _attend_check(c, 2.0)
+
+
+def test_attend_broadcast_queries_and_one_pool():
+    """Every token with the same queries (a stride of zero), keys that are their own values."""
+    c = pc.paged_inputs(16, [90, 40], [3, 2], 4, 2, 64, 16, BF)
+    same = dict(c, q=c["q"][:1].expand(5, 4, 64), v_pool=c["k_pool"])
+    _attend_check(same, 0.125)
+    _attend_check(dict(same, q=same["q"].contiguous()), 0.125)
+
+
+def test_what_a_page_shared_by_two_requests_holds():
+    """A prefix that two requests share: the same pages in both rows of the table."""
+    c = pc.paged_inputs(17, [64, 100], [1, 1], 4, 2, 64, 16, BF)
+    c["table"][1][:3] = c["table"][0][:3]
+    c["d_table"] = _i32(c["table"])
+    _attend_check(c, 0.125)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_write_and_rotary_on_another_stream(dtype):
+    side = torch.cuda.Stream()
+    x = torch.randn(50, 4, 64, device="cuda").to(dtype)
+    pos, freq = torch.arange(50, dtype=torch.int32, device="cuda"), _freqs(32)
+    pools = [torch.zeros(8, 4, 16, 64, device="cuda", dtype=dtype) for _ in range(4)]
+    slots = torch.randperm(128, device="cuda")[:50].to(torch.int32)
+    want = wc.rotary(x, pos, freq, (32,))
+    wc.paged_write(x, x, slots, pools[0], pools[1], positions=pos, inv_freq=freq, sections=(32,))
+    torch.cuda.synchronize()
+    got = wc.rotary(x, pos, freq, (32,), stream=side)
+    wc.paged_write(x, x, slots, pools[2], pools[3], positions=pos, inv_freq=freq, sections=(32,), stream=side)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
