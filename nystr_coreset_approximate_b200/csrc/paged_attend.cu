@@ -151,7 +151,8 @@ __device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* 
         for (int k = 0; k < 4; ++k) v[k] *= a.scale;
         *reinterpret_cast<float4*>(Qs + r * QS + c) = make_float4(v[0], v[1], v[2], v[3]);
     }
-    float acc[RT][CH][CW], m[RT], l[RT];
+    float2 acc[RT][CH][CW / 2];
+    float m[RT], l[RT];
     int end[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -162,7 +163,7 @@ __device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* 
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-            for (int k = 0; k < CW; ++k) acc[r][c][k] = 0.f;
+            for (int k = 0; k < CW / 2; ++k) acc[r][c][k] = make_float2(0.f, 0.f);
     }
     Rows<E, D> rows;
     rows.fetch(a, g, a.K, a.k_p, a.k_h, a.k_r, g.t0 * kN);
@@ -173,10 +174,11 @@ __device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* 
         rows.fetch(a, g, a.V, a.v_p, a.v_h, a.v_r, k0);
         __syncthreads();
         float s[RT][4];
+        float2 s2[RT][4];  // over even and odd columns: packed multiply-adds
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[r][k] = 0.f;
+            for (int k = 0; k < 4; ++k) s2[r][k] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int c = 0; c < D; c += 4) {
             float4 kv[4];
@@ -187,13 +189,15 @@ __device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* 
                 const float4 q = *reinterpret_cast<const float4*>(Qs + (ty * RT + r) * QS + c);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    s[r][k] = fmaf(q.x, kv[k].x, s[r][k]);
-                    s[r][k] = fmaf(q.y, kv[k].y, s[r][k]);
-                    s[r][k] = fmaf(q.z, kv[k].z, s[r][k]);
-                    s[r][k] = fmaf(q.w, kv[k].w, s[r][k]);
+                    s2[r][k] = tc::ffma2(make_float2(q.x, q.y), make_float2(kv[k].x, kv[k].y), s2[r][k]);
+                    s2[r][k] = tc::ffma2(make_float2(q.z, q.w), make_float2(kv[k].z, kv[k].w), s2[r][k]);
                 }
             }
         }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[r][k] = s2[r][k].x + s2[r][k].y;
         __syncthreads();  // K has been read: V takes its place
         rows.store(KVs);
         if (kt + 1 < g.t1) rows.fetch(a, g, a.K, a.k_p, a.k_h, a.k_r, k0 + kN);
@@ -223,7 +227,10 @@ __device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* 
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int k = 0; k < CW; ++k) acc[r][c][k] *= f;
+                for (int k = 0; k < CW / 2; ++k) {
+                    acc[r][c][k].x *= f;
+                    acc[r][c][k].y *= f;
+                }
         }
         __syncthreads();
 #pragma unroll 2
@@ -235,20 +242,20 @@ __device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* 
             for (int jj = 0; jj < 4; ++jj) {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    float v[CW];
+                    float2 v[CW / 2];
                     const float* src = KVs + (j + jj) * QS + c * 64 + tx * CW;
                     if constexpr (CW == 4) {
                         const float4 x = *reinterpret_cast<const float4*>(src);
-                        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+                        v[0] = make_float2(x.x, x.y);
+                        v[1] = make_float2(x.z, x.w);
                     } else {
-                        const float2 x = *reinterpret_cast<const float2*>(src);
-                        v[0] = x.x; v[1] = x.y;
+                        v[0] = *reinterpret_cast<const float2*>(src);
                     }
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
                         const float pr = jj == 0 ? p[r].x : jj == 1 ? p[r].y : jj == 2 ? p[r].z : p[r].w;
 #pragma unroll
-                        for (int k = 0; k < CW; ++k) acc[r][c][k] = fmaf(pr, v[k], acc[r][c][k]);
+                        for (int k = 0; k < CW / 2; ++k) acc[r][c][k] = tc::ffma2(make_float2(pr, pr), v[k], acc[r][c][k]);
                     }
                 }
             }
@@ -267,7 +274,10 @@ __device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* 
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int k = 0; k < CW; ++k) put(o + c * 64 + tx * CW + k, acc[r][c][k] * rcp);
+                for (int k = 0; k < CW / 2; ++k) {
+                    put(o + c * 64 + tx * CW + 2 * k, acc[r][c][k].x * rcp);
+                    put(o + c * 64 + tx * CW + 2 * k + 1, acc[r][c][k].y * rcp);
+                }
             if (a.lse && tx == 0)
                 a.lse[(int64_t)(first + i) * (a.s.Hkv * a.s.g) + hq] =
                     l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * 0.6931471805599453f;
@@ -276,7 +286,7 @@ __device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* 
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int k = 0; k < CW; ++k) o[c * 64 + tx * CW + k] = acc[r][c][k];
+                for (int k = 0; k < CW / 2; ++k) *reinterpret_cast<float2*>(o + c * 64 + tx * CW + 2 * k) = acc[r][c][k];
             if (tx == 0) a.p.ml[piece + x] = make_float2(m[r], l[r]);
         }
     }
