@@ -12,8 +12,8 @@
 // float32 and for bf16 in shapes that the tensor cores' copies do not take
 // (d = 32, a page that is no multiple of 8 rows, strides that are no multiple
 // of 16 bytes).  It works in float32 throughout: one row tile is 64 rows, or 16
-// where the unit has no more (a decoded token), against 64 keys; a thread holds
-// 4 x 4 (1 x 4) scores and 4 (1) rows of D / 16 accumulators, in packed pairs.  A
+// where the unit has no more, against 64 keys (units of up to four rows go without
+// tiles); a thread holds 4 x 4 (1 x 4) scores and 4 (1) rows of D / 16 accumulators, in packed pairs.  A
 // tile of 64 rows takes 8,000 cycles of an SM that has two blocks (4,096 of them
 // multiply-adds, 3,000 reads of shared memory): 900 new tokens of two requests in
 // 169 us at d = 128 (20 TFLOP/s), 32 decoded ones over 4,000 keys in 300 us.
@@ -295,6 +295,126 @@ __device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* 
     }
 }
 
+// One segment of a unit of up to kFew rows (a decoded token of a few query heads): no
+// tiles, since 16 rows of threads would idle behind as many reads of shared memory
+// (11,600 cycles for 64 keys).  D / 4 lanes make a stream that takes every kStreams-th
+// key, straight from memory to registers, four keys at a time, with a running maximum,
+// sum and accumulators of its own; the streams are joined in shared memory, in order.
+constexpr int kFew = 4;
+template <typename E, int D>
+__device__ void simt_few(const SimtArgs& a, const Seg& g, float* sm) {
+    using T = typename E::T;
+    constexpr int LN = D / 4, kStreams = kThreads / LN, U = 4;
+    const int tid = threadIdx.x, col = tid % LN * 4, stream = tid / LN;
+    const int first = a.s.first_row(g.b);
+    float q[kFew][4], acc[kFew][4], m[kFew], l[kFew];
+    int end[kFew];
+#pragma unroll
+    for (int r = 0; r < kFew; ++r) {
+        const int x = g.row0 + r, i = x / a.s.g;
+        end[r] = r >= g.rows ? 0 : (a.s.causal ? g.L - g.n + i + 1 : g.L);
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[r][k] = acc[r][k] = 0.f;
+        if (r < g.rows)
+            load4<T>(static_cast<const T*>(a.Q) + (int64_t)(first + i) * a.q_t + (int64_t)(g.h * a.s.g + x - i * a.s.g) * a.q_h + col,
+                     a.wide, q[r]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[r][k] *= a.scale;
+    }
+    const T* K = static_cast<const T*>(a.K) + (int64_t)g.h * a.k_h + col;
+    const T* V = static_cast<const T*>(a.V) + (int64_t)g.h * a.v_h + col;
+    const int32_t* tab = a.s.table + (int64_t)g.b * a.s.table_stride;
+    const int hi = min(g.t1 * kN, g.L);
+    bool bad = false;
+    for (int j0 = g.t0 * kN + stream; j0 - stream < hi; j0 += U * kStreams) {  // the same number of turns for all
+        int id[U];
+        float k4[U][4], v4[U][4], s[kFew][U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * kStreams;
+            id[u] = j < hi ? __ldg(tab + (unsigned)j / (unsigned)a.s.page_size) : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * kStreams, at = (unsigned)j % (unsigned)a.s.page_size;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) k4[u][k] = v4[u][k] = 0.f;
+            if (j < hi) {
+                if (id[u] >= 0 && id[u] < a.s.pages) {
+                    load4<T>(K + (int64_t)id[u] * a.k_p + (int64_t)at * a.k_r, a.wide, k4[u]);
+                    load4<T>(V + (int64_t)id[u] * a.v_p + (int64_t)at * a.v_r, a.wide, v4[u]);
+                } else {
+                    bad = true;
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kFew; ++r) {
+            if (r >= g.rows) break;
+            float best = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float x = q[r][0] * k4[u][0];
+#pragma unroll
+                for (int k = 1; k < 4; ++k) x = fmaf(q[r][k], k4[u][k], x);
+#pragma unroll
+                for (int o = LN / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                s[r][u] = j0 + u * kStreams < min(end[r], hi) ? x : -INFINITY;
+                best = fmaxf(best, s[r][u]);
+            }
+            const float mn = fmaxf(m[r], best), base = mn == -INFINITY ? 0.f : mn, f = exp2f(m[r] - base);
+            m[r] = mn;
+            l[r] *= f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[r][k] *= f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float p = exp2f(s[r][u] - base);
+                l[r] += p;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[r][k] = fmaf(p, v4[u][k], acc[r][k]);
+            }
+        }
+    }
+    if (bad) atomicMax(&g_paged_attend_status, 1);
+    float2* ml = reinterpret_cast<float2*>(sm + kStreams * kFew * D);
+    __syncthreads();  // the previous segment's reads are done
+#pragma unroll
+    for (int r = 0; r < kFew; ++r) {
+        *reinterpret_cast<float4*>(sm + (stream * kFew + r) * D + col) = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+        if (col == 0) ml[stream * kFew + r] = make_float2(m[r], l[r]);
+    }
+    __syncthreads();
+    const bool whole = g.t0 == 0 && g.t1 == g.nt;
+    const int64_t piece = ((int64_t)blockIdx.x * 2 + (g.t0 > 0 ? 0 : 1)) * kM;
+    for (int e = tid; e < g.rows * D; e += kThreads) {
+        const int r = e / D, c = e - r * D;
+        float top = -INFINITY;
+        for (int x = 0; x < kStreams; ++x) top = fmaxf(top, ml[x * kFew + r].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = 0.f, out = 0.f;
+        for (int x = 0; x < kStreams; ++x) {
+            const float2 w = ml[x * kFew + r];
+            const float f = exp2f(w.x - base);
+            sum = fmaf(f, w.y, sum);
+            out = fmaf(f, sm[(x * kFew + r) * D + c], out);
+        }
+        if (whole) {
+            const int i = (g.row0 + r) / a.s.g, hq = g.h * a.s.g + g.row0 + r - i * a.s.g;
+            put(static_cast<T*>(a.O) + (int64_t)(first + i) * a.o_t + (int64_t)hq * a.o_h + c,
+                sum > 0.f || sum != sum ? out / sum : 0.f);
+            if (a.lse && c == 0)
+                a.lse[(int64_t)(first + i) * (a.s.Hkv * a.s.g) + hq] =
+                    sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        } else {
+            a.p.part[(piece + r) * D + c] = out;
+            if (c == 0) a.p.ml[piece + r] = make_float2(top, sum);
+        }
+    }
+}
+
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     extern __shared__ __align__(16) float simt_sm[];
@@ -310,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
         w.start(a.s, scratch.share);
         Seg g;
         while (w.next(a.s, g)) {
-            if (g.rows <= 16) simt_segment<E, D, 1>(a, g, Qs, KVs, Ps);
+            if (g.rows <= kFew) simt_few<E, D>(a, g, simt_sm);
+            else if (g.rows <= 16) simt_segment<E, D, 1>(a, g, Qs, KVs, Ps);
             else simt_segment<E, D, 4>(a, g, Qs, KVs, Ps);
             if (g.t0 > 0 && g.t1 == g.nt) join = make_int4(g.b, g.h, g.t, scratch.share.line.block(g.first_end));
         }
