@@ -158,15 +158,15 @@ struct Seg {
     int64_t first_end;           // the last place of the unit's first key tile
 };
 
-// The T places in all and the blocks that share them.  Each has enough places for a key
-// tile to end in it (a unit has more than that).
+// The T places in all and the blocks that share them.  Each of several has enough places
+// for a key tile to end in it.
 struct Line {
     int64_t total, each;  // places of a block, and one more for the first `rest` of them
     int active, rest;
 
     __device__ __forceinline__ void of(const Shape& s, int64_t t, int G) {
         total = t;
-        active = (int)min(t >> s.wide, (int64_t)G);
+        active = (int)min(max(t >> s.wide, (int64_t)(t > 0)), (int64_t)G);
         each = active > 0 ? quotient(t, active) : 0;
         rest = (int)(t - each * active);
     }

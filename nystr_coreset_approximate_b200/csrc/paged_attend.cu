@@ -448,7 +448,7 @@ Status run_simt(const PagedAttendRequest& q, cudaStream_t st) {
     carve_plan(cv, &a.p, G, kM, D);
     if (!cv.fits()) return Status::fail(4, "paged_attend: workspace too small");
     a.s = Shape{q.table, q.table_stride, q.W, q.seq_lens, q.cu_new, q.T, q.pages, (int)q.B, q.Hkv, q.Hq / q.Hkv,
-                q.page_size, kM, 16, 1, q.causal};
+                q.page_size, kM, kFew, 2, q.causal};
     a.Q = q.Q; a.K = q.K; a.V = q.V;
     a.q_t = q.q_t; a.q_h = q.q_h;
     a.k_p = q.k_p; a.k_h = q.k_h; a.k_r = q.k_r;
