@@ -356,7 +356,8 @@ wildcat_status wildcat_paged_write(const void* k, int64_t k_token, int64_t k_hea
  *   k_pool, v_pool  [pages, Hkv, page_size, d], HOST strides {page, head, row}
  *   seq_lens [B], cu_new [B + 1] int32, cu_new[0] = 0
  *   beta   softmax scale (> 0, finite)
- *   O      out [T, Hq, d], dtype `dtype`, element strides o_token and o_head
+ *   O      out [T, Hq, d], dtype `dtype`, element strides o_token and o_head; may
+ *          be Q itself with the same strides
  *   lse    out [T, Hq] float32 log of the sum of exponentials (-inf for rows that
  *          see no key), or NULL
  *   workspace >= wildcat_paged_attend_workspace_size(B, d) bytes; two calls that

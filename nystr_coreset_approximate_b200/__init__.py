@@ -788,8 +788,8 @@ def paged_attend(q, k_pool, v_pool, block_table, seq_lens, cu_new, beta: float, 
     of its pages block_table[b].  causal: token i of n sees the first
     seq_lens[b] - n + i + 1 of them, else all see all (an encoder's states).
     Hq is a multiple of the pools' heads.  A row that sees no key is zero.
-    Returns O [T, Hq, d] in q's dtype (rows at or past cu_new[B] are not
-    written); lse, a float32 [T, Hq] tensor, receives the logs of the sums of
+    Returns O [T, Hq, d] in q's dtype (in `out`, which may be q; rows at or past
+    cu_new[B] are not written); lse, a float32 [T, Hq] tensor, receives the logs of the sums of
     exponentials."""
     torch = _torch()
     i32 = torch.int32

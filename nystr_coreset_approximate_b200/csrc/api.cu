@@ -1062,6 +1062,8 @@ wildcat_status wildcat_paged_attend(const void* Q, int64_t q_token, int64_t q_he
         for (int i = 0; i < 3; ++i)
             if (s[i] < 0) return bad(1, "%s: strides must be >= 0", who);
     if ((T > 1 && o_token < d) || (Hq > 1 && o_head < d)) return bad(1, "%s: rows of O overlap", who);
+    if (Q == O && ((T > 1 && q_token != o_token) || (Hq > 1 && q_head != o_head)))
+        return bad(1, "%s: in place, Q and O must have the same strides", who);
     for (const void* p : {Q, k_pool, v_pool, (const void*)O})
         if (!elem_aligned(p, dtype)) return bad(1, "%s: tensors must be aligned to their elements", who);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return bad(4, "%s: workspace must be 256-byte aligned", who);

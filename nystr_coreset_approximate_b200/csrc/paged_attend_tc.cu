@@ -948,7 +948,7 @@ bool paged_attend_tc_supported(const PagedAttendRequest& q) {
                            reinterpret_cast<uintptr_t>(q.V) | reinterpret_cast<uintptr_t>(q.O);
     return q.dtype == 1 && (q.d == 64 || q.d == 128) && q.pages > 0 && g <= kRows &&
            (ps % kKeys == 0 || (kKeys % ps == 0 && ps % 8 == 0)) && (ptrs & 15u) == 0 && map_stride(q.T, q.q_t) &&
-           map_stride(q.Hq, q.q_h) && q.q_h < (int64_t(1) << 32) && map_stride(ps, q.k_r) && map_stride(q.Hkv, q.k_h) &&
+           map_stride(q.Hq, q.q_h) && q.q_h < (int64_t(1) << 31) && map_stride(ps, q.k_r) && map_stride(q.Hkv, q.k_h) &&
            map_stride(q.pages, q.k_p) && map_stride(ps, q.v_r) && map_stride(q.Hkv, q.v_h) && map_stride(q.pages, q.v_p) &&
            (q.T <= 1 || q.o_t % 8 == 0) && (q.Hq <= 1 || q.o_h % 8 == 0);
 }

@@ -541,3 +541,21 @@ def test_attend_infinities_behind_the_length(dtype):
     for p in (c["k_pool"], c["v_pool"]):
         p[p.isinf()] = math.inf
     assert torch.equal(_attend(c, 0.125), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lens,new", [([300, 40], [300, 1]), ([5000, 2000, 9], [1, 1, 1])], ids=str)
+def test_attend_in_place(dtype, lens, new):
+    """O over Q: other blocks may still hold parts of a row's work when its first result is written."""
+    c = pc.paged_inputs(20, lens, new, 4, 2, 64, 16, dtype, nan=False)
+    want = _attend(c, 0.125)
+    for _ in range(5):
+        q = c["q"].clone()
+        assert _attend(dict(c, q=q), 0.125, out=q) is q and torch.equal(q, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,d", [(1, 1, 32), (2, 1, 64), (3, 1, 128), (4, 1, 64), (5, 1, 128)], ids=str)
+def test_attend_few_rows_in_odd_pages(dtype, Hq, Hkv, d):
+    """Units of one to five rows, also two tokens of two heads, over pages that divide nothing."""
+    _attend_check(pc.paged_inputs(21, [700, 1, 65, 130], [1, 1, 2, 1], Hq, Hkv, d, 7, dtype), 1 / math.sqrt(d))

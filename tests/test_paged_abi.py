@@ -89,7 +89,7 @@ def _attend_defaults():
     (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(Hq=65538), 2), (dict(T=1 << 30), 2), (dict(W=1 << 31, stride=1 << 31), 2), (dict(q=None), 1),
     (dict(kp=None), 1), (dict(vp=None), 1), (dict(ks=None), 1), (dict(vs=None), 1), (dict(table=None), 1), (dict(lens=None), 1),
     (dict(cu=None), 1), (dict(out=None), 1), (dict(ws=None), 1), (dict(qt=-1), 1), (dict(ks=_longs(2048, -1, 64)), 1), (dict(ot=10), 1),
-    (dict(oh=10), 1), (dict(ws=ctypes.c_void_p((1 << 20) + 64)), 4), (dict(n=4096), 4), (dict(q=ctypes.c_void_p(4097)), 1),
+    (dict(oh=10), 1), (dict(out=FAKE, ot=512), 1), (dict(out=FAKE, ot=512, oh=128), 1), (dict(ws=ctypes.c_void_p((1 << 20) + 64)), 4), (dict(n=4096), 4), (dict(q=ctypes.c_void_p(4097)), 1),
 ], ids=lambda k: str(k)[:40])
 def test_paged_attend_refuses(kw, code):
     assert _call("wildcat_paged_attend", _attend_defaults(), kw) == code
