@@ -19,9 +19,9 @@
 //   memory for all heads; the angle is reduced to a fraction of a turn in
 //   double (positions run far: in float32 a position of 10^5 would leave the
 //   angle off by 10^-2), the rest is float32, rounded once at the end.  31,104 x 16
-//   rows of 128 float32 take 84 us (6.1 TB/s, 0.93 of a copy's rate); keys, values
-//   and queries of a 16,383-token prompt into random slots 63 us (4.8 TB/s: rows of
-//   256 bytes; two units in flight per thread instead of one gave 65.8 us).
+//   rows of 128 float32 take 82 us (6.2 TB/s, 0.95 of a copy's rate); keys, values
+//   and queries of a 16,383-token prompt into random slots 60 us (5.0 TB/s: rows of
+//   256 bytes; two units in flight per thread instead of one cost 3 us more).
 #include <algorithm>
 
 #include "common.cuh"
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesRequest 
 }
 
 // ------------------------------------------------------------ rotary and writes
-constexpr int kTurnThreads = 256;
+constexpr int kTurnThreads = 128;
 
 template <int VEC>
 __device__ __forceinline__ void load_vec(const float* p, float (&v)[VEC]) {
@@ -364,11 +364,12 @@ __global__ void __launch_bounds__(kTurnThreads) turn_kernel(TurnRequest q, int t
 
 template <typename E, int VEC>
 Status run_turn(const TurnRequest& q, cudaStream_t st) {
-    // tokens of a block: about 64 KB of rows, so that the angles are formed once for
-    // many heads, but at least two blocks for each SM where there are tokens enough
+    // tokens of a block: about 32 KB of rows, so that the angles are formed once for
+    // many heads, but at least two blocks for each SM where there are tokens enough (a
+    // 16,383-token prompt's write 60 us; 64 KB in blocks of 256 threads 63, 24 KB 61)
     const int64_t heads = q.part[0].heads + q.part[1].heads + q.part[2].heads;
     const int64_t row = heads * q.d * (int64_t)sizeof(typename E::T);
-    int64_t tpb = std::max<int64_t>(1, std::min<int64_t>(65536 / std::max<int64_t>(row, 1), q.T / 296));
+    int64_t tpb = std::max<int64_t>(1, std::min<int64_t>(32768 / std::max<int64_t>(row, 1), q.T / 296));
     if (q.half > 0) tpb = std::min<int64_t>(tpb, std::max<int64_t>(1, 4096 / q.half));
     const size_t smem = sizeof(float2) * (size_t)tpb * q.half;
     const int64_t grid = ceil_div(q.T, tpb);
