@@ -26,6 +26,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "paged.cuh"
 
 namespace wildcat {
 
@@ -385,11 +386,10 @@ Status run_turn(const TurnRequest& q, cudaStream_t st) {
 Status launch_page_tables(const TablesRequest& q, cudaStream_t st) {
     if (q.B > kTabMaxB) return Status::fail(2, "page_tables: more than 16384 requests");
     const size_t smem = sizeof(int) * 3 * (size_t)(q.B + 1);
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return Status::cuda(e, "page_tables: shared memory attribute");
-    }
+    // for the most requests at once, whatever this call needs: the attribute belongs to the
+    // function, and 48 KB without it cover the kernel's static shared memory too
+    const cudaError_t a = paged::allow_smem<page_tables_kernel>((int)sizeof(int) * 3 * (kTabMaxB + 1));
+    if (a != cudaSuccess) return Status::cuda(a, "page_tables: shared memory attribute");
     const int64_t work = std::max<int64_t>(q.max_tokens, 1);
     const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(work, kTabThreads), 148);
     page_tables_kernel<<<grid, kTabThreads, smem, st>>>(q);
