@@ -268,10 +268,20 @@ wildcat_status wildcat_decode_attend(const void* Q_new, const void* K_new, const
  * pages of a request that ends go behind the ring's last page (to be handed out
  * by later calls); its row is left as it is.
  *
+ * A page id that is none (below zero, or with slots past 2^31) makes no slot:
+ * its tokens get slot -1.  It stands in the table, or goes back onto the ring,
+ * like any other and takes a place there.  A cached length below zero counts as
+ * zero; a request with more tokens cached than its row has pages does not
+ * advance, and gives back W pages when it ends; the ring's first place counts
+ * modulo P, its free pages from 0 to P; pages that come back and find no room
+ * on it are lost.  Each of these leaves WILDCAT_ERR_INVALID_ARG in the device
+ * status.  (A page id past the pool is found by the calls that know the pool.)
+ *
  *   ctx_lens, new_lens  [B] int32, B <= 16384
  *   block_table  in/out [B, W] int32, rows table_stride entries apart; only the
  *                entries of pages handed out are written
- *   free_ring    in/out [P] int32 page ids (P the pool's pages)
+ *   free_ring    in/out [P] int32 page ids, P at least the pages that are handed out
+ *                and come back (the pool's, or a part of them)
  *   ring_state   [2] int32: place of the first free page in the ring, free pages
  *   seq_lens     out [B] int32 lengths after the step (0 for a request that ends)
  *   cu_new       out [B + 1] int32 new tokens before each request
@@ -553,9 +563,9 @@ wildcat_status wildcat_pivot_uniforms(uint64_t seed, int64_t BH, int steps, doub
  * copies in flight, releases its tensor memory and returns, leaving its
  * output incomplete (the select stops every CTA of the instance at the same
  * step and reports the steps taken as the rank).
- * The paged calls record WILDCAT_ERR_INVALID_ARG there for slots, page ids and
- * lengths in device memory that lie outside their tensors (such accesses are
- * skipped).  Returns WILDCAT_OK, WILDCAT_ERR_TIMEOUT, WILDCAT_ERR_INVALID_ARG, or
+ * The paged calls record WILDCAT_ERR_INVALID_ARG there for slots, page ids,
+ * lengths and ring states in device memory that lie outside their tensors (such
+ * accesses are skipped).  Returns WILDCAT_OK, WILDCAT_ERR_TIMEOUT, WILDCAT_ERR_INVALID_ARG, or
  * WILDCAT_ERR_CUDA if the stream or the status word could not be read.
  */
 wildcat_status wildcat_get_device_status(void* stream);

@@ -637,7 +637,8 @@ def page_tables(ctx_lens, new_lens, block_table, free_ring, ring_state, page_siz
     (-1: it ends).  New pages come off free_ring [P] at ring_state = (first
     free place, free pages) and go into block_table [B, W]; pages of requests
     that end go back to the ring; both tensors are updated in place.  A
-    request gets all the pages it needs or does not advance.
+    request gets all the pages it needs or does not advance.  Ids that are no
+    page's, lengths and ring states out of range show in device_status().
 
     Returns (seq_lens [B], cu_new [B + 1], positions [max_tokens],
     slots [max_tokens], ring_out [4]): ring_out[:2] is the next call's
@@ -842,8 +843,8 @@ def pivot_uniforms(seed: int, BH: int, steps: int, device="cuda"):
 
 def device_status(stream=None) -> int:
     """Wait for the stream, then return and clear the device status word
-    (0 = fine, 1 = a paged call met a slot, page id or length outside its
-    tensor, 5 = a kernel's bounded wait expired)."""
+    (0 = fine, 1 = a paged call met a slot, page id, length or ring state
+    outside its tensor, 5 = a kernel's bounded wait expired)."""
     return int(lib().wildcat_get_device_status(_stream(stream)))
 
 

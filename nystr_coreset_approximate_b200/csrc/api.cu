@@ -807,7 +807,7 @@ wildcat_status wildcat_get_device_status(void* stream) {
     if (v < 0) return record(Status::fail(3, "wildcat_get_device_status: cannot read the status word"));
     if (v == WILDCAT_ERR_TIMEOUT) return record(Status::fail(5, "a kernel's bounded wait expired"));
     if (v == WILDCAT_ERR_INVALID_ARG)
-        return record(Status::fail(1, "a kernel met a slot, page id or length outside its tensor"));
+        return record(Status::fail(1, "a kernel met a slot, page id, length or ring state outside its tensor"));
     return record(Status::ok());
 }
 

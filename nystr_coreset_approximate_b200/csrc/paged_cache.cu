@@ -30,7 +30,7 @@
 
 namespace wildcat {
 
-__device__ int g_paged_status = 0;  // WILDCAT_ERR_INVALID_ARG when a slot lies outside the pool
+__device__ int g_paged_status = 0;  // WILDCAT_ERR_INVALID_ARG: a slot, page id, length or ring state out of range
 
 namespace {
 
@@ -103,11 +103,18 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesRequest 
     const int tid = threadIdx.x;
     const int64_t page = q.page_size;
     const int P = (int)q.P;
+    // A page's slots are id page .. id page + page - 1, and fit in 32 bits up to this id: a
+    // larger one (or one below zero) is no page of any pool, and in 32 bits its slots would be
+    // another page's.
+    const int most_id = (int)(0x80000000u / (unsigned)q.page_size - 1u);
+    auto no_page = [&](int id) { return id < 0 || id > most_id; };
+    bool bad = false;  // an id, a length or the ring's state is out of range
     int head = 0, count = 0;
     if (P > 0) {
         head = q.ring_state[0] % P;
         if (head < 0) head += P;
         count = min(max(q.ring_state[1], 0), P);
+        bad = head != q.ring_state[0] || count != q.ring_state[1];
     }
     if (tid < 2) totals[tid] = 0;
     // prefix sums over the requests, kTabThreads of them at a time
@@ -169,6 +176,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesRequest 
             if (b == B) break;
             const int64_t ctx = max(q.ctx_lens[b], 0);
             const int n = q.new_lens[b];
+            bad = bad || q.ctx_lens[b] < 0 || (ctx + page - 1) / page > q.W;
             const bool adv = advances(b, ctx, n);
             q.seq_lens[b] = n < 0 ? 0 : (int)(adv ? ctx + n : ctx);
             if (adv && first[b + 1] > first[b]) taken = max(taken, first[b + 1]);
@@ -180,6 +188,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesRequest 
         __syncthreads();
         if (tid == 0) {
             const int give = min(gfirst[B], P - count);
+            bad = bad || give < gfirst[B];
             q.ring_out[0] = P > 0 ? (int)(((int64_t)head + totals[0]) % P) : 0;
             q.ring_out[1] = count - totals[0] + give;
             q.ring_out[2] = first[B] - totals[0];
@@ -201,7 +210,8 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesRequest 
                 // written by another thread
                 const int id = p < have ? q.table[b * q.table_stride + p]
                                         : q.ring[((int64_t)head + first[b] + (p - have)) % P];
-                if (id >= 0) slot = (int)((int64_t)id * page + x % page);
+                if (no_page(id)) bad = true;
+                else slot = (int)((int64_t)id * page + x % page);
             }
         }
         q.positions[t] = pos;
@@ -213,13 +223,18 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesRequest 
         const int64_t ctx = max(q.ctx_lens[b], 0);
         if (first[b + 1] > count) continue;
         const int64_t have = (ctx + page - 1) / page;
-        q.table[b * q.table_stride + have + (k - first[b])] = q.ring[((int64_t)head + k) % P];
+        const int id = q.ring[((int64_t)head + k) % P];
+        bad = bad || no_page(id);
+        q.table[b * q.table_stride + have + (k - first[b])] = id;
     }
     // pages given back: never onto the entries read above (those are the ring's filled part)
     for (int k = at; k < min(gfirst[B], P - count); k += stride) {
         const int b = range_of(gfirst, B, k);
-        q.ring[((int64_t)head + count + k) % P] = q.table[b * q.table_stride + (k - gfirst[b])];
+        const int id = q.table[b * q.table_stride + (k - gfirst[b])];
+        bad = bad || no_page(id);
+        q.ring[((int64_t)head + count + k) % P] = id;
     }
+    if (bad) atomicMax(&g_paged_status, 1);
 }
 
 // ------------------------------------------------------------ rotary and writes
@@ -314,7 +329,7 @@ __global__ void __launch_bounds__(kTurnThreads) turn_kernel(TurnRequest q, int t
             if (slot < 0) continue;
             const int page = slot / q.page_size;
             if (page >= q.pages) {
-                atomicExch(&g_paged_status, 1);
+                atomicMax(&g_paged_status, 1);
                 continue;
             }
             dst += (int64_t)page * p.dst_t + (int64_t)h * p.dst_h + (int64_t)(slot - page * q.page_size) * p.dst_r;

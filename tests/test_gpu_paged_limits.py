@@ -1,5 +1,6 @@
 """The exact paged cache at its limits: the most requests that page_tables
-takes, and calls of different sizes from two host threads."""
+takes, calls of different sizes from two host threads, and tables and rings whose
+contents are out of range."""
 import threading
 
 import pytest
@@ -66,3 +67,52 @@ def test_tables_of_two_sizes_from_two_threads():
         t.join()
     assert not failed, failed
     assert wc.device_status() == 0
+
+
+# ------------------------------------------------- ids, lengths and rings that are no such thing
+def _bad_call(ctx, new, table, ring, head, count, page=4, T=6):
+    d_table, d_ring = _i32(table), _i32(ring)
+    got = wc.page_tables(_i32(ctx), _i32(new), d_table, d_ring, _i32([head, count]), page, T)
+    out = [g.tolist() for g in got], d_table.tolist(), d_ring.tolist()
+    return (*out, wc.device_status(), wc.device_status())
+
+
+# 2^29 pages of 4 rows are 2^31 slots: the first two wrap to slots of page 0 in 32 bits
+@pytest.mark.parametrize("bad", [2 ** 30, 2 ** 30 + 1, 2 ** 29, 2 ** 31 - 1, -1, -5], ids=str)
+def test_tables_make_no_slot_of_a_bad_id(bad):
+    # cached pages: the last one of request 0 is bad; request 1 is as it should be
+    (seq, cu, pos, slots, state), *_, status, again = _bad_call([6, 3], [2, 1], [[3, bad, -1], [5, -1, -1]], [7, 8, 9, -1], 0, 3)
+    assert (seq, cu, pos[:3], state) == ([8, 4], [0, 2, 3], [6, 7, 3], [0, 3, 0, 0])
+    assert slots == [-1, -1, 23, -1, -1, -1] and (status, again) == (1, 0)
+    # a page off the ring
+    (seq, _, _, slots, state), table, _, status, again = _bad_call([4, 4], [2, 1], [[3, -1], [5, -1]], [bad, 8, 9, -1], 0, 3)
+    assert slots == [-1, -1, 32, -1, -1, -1] and state == [2, 1, 0, 0] and (status, again) == (1, 0)
+    assert table == [[3, bad], [5, 8]]
+
+
+def test_tables_take_the_last_id_whose_slots_fit():
+    (_, _, _, slots, _), *_, status, _ = _bad_call([6], [2], [[3, 2 ** 29 - 1]], [7], 0, 1)
+    assert slots == [2 ** 31 - 2, 2 ** 31 - 1, -1, -1, -1, -1] and status == 0
+    (_, _, _, slots, _), *_, status, _ = _bad_call([1], [1], [[3, -1]], [2 ** 31 - 1], 0, 1, page=1)
+    assert slots == [2 ** 31 - 1, -1, -1, -1, -1, -1] and status == 0
+
+
+def test_tables_report_a_bad_id_that_comes_back():
+    (seq, _, _, _, state), _, ring, status, again = _bad_call([6, 1], [-1, 0], [[3, -1, -1], [5, -1, -1]], [7, 8, 9, 0], 1, 2)
+    assert seq == [0, 1] and state == [1, 4, 0, 0] and ring == [-1, 8, 9, 3] and (status, again) == (1, 0)
+
+
+@pytest.mark.parametrize("ctx,new,ring,head,count,what", [
+    ([-3, 2], [1, 1], [7, 8], 0, 2, ([1, 3], [7 * 4, 5 * 4 + 2], [1, 1, 0, 0])),  # a length below zero counts as zero
+    ([2, 2], [1, 1], [7, 8], 0, 3, ([3, 3], [14, 22], [0, 2, 0, 0])),  # more free pages than the ring has places
+    ([2, 2], [1, 1], [7, 8], 0, -1, ([3, 3], [14, 22], [0, 0, 0, 0])),
+    ([4, 2], [1, 1], [7, 8], 2, 2, ([5, 3], [28, 22], [1, 1, 0, 0])),  # a first place outside the ring: modulo its size
+    ([4, 2], [1, 1], [7, 8], -1, 2, ([5, 3], [32, 22], [0, 1, 0, 0])),
+    ([9, 2], [0, 1], [7, 8], 0, 2, ([9, 3], [22], [0, 2, 0, 1])),  # more tokens cached than the row has pages
+    ([9, 2], [-1, 1], [7, 8, 0, 0], 0, 2, ([0, 3], [22], [0, 4, 0, 0])),
+    ([8, 2], [-1, 1], [7, 8, 0], 0, 2, ([0, 3], [22], [0, 3, 0, 0])),  # more pages come back than the ring has room for
+], ids=str)
+def test_tables_report_lengths_and_rings_out_of_range(ctx, new, ring, head, count, what):
+    (seq, cu, _, slots, state), *_, status, again = _bad_call(ctx, new, [[3, 4], [5, 6]], ring, head, count)
+    assert (seq, slots[:cu[-1]], state) == what
+    assert (status, again) == (1, 0)
