@@ -566,7 +566,9 @@ wildcat_status wildcat_pivot_uniforms(uint64_t seed, int64_t BH, int steps, doub
  * The paged calls record WILDCAT_ERR_INVALID_ARG there for slots, page ids,
  * lengths and ring states in device memory that lie outside their tensors (such
  * accesses are skipped).  Returns WILDCAT_OK, WILDCAT_ERR_TIMEOUT, WILDCAT_ERR_INVALID_ARG, or
- * WILDCAT_ERR_CUDA if the stream or the status word could not be read.
+ * WILDCAT_ERR_CUDA if the stream or the status word could not be read, or if a
+ * kernel could not run as built and left its output unwritten.  Where several
+ * apply: an expired wait first, bad data last.
  */
 wildcat_status wildcat_get_device_status(void* stream);
 

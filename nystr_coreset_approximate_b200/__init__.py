@@ -844,7 +844,8 @@ def pivot_uniforms(seed: int, BH: int, steps: int, device="cuda"):
 def device_status(stream=None) -> int:
     """Wait for the stream, then return and clear the device status word
     (0 = fine, 1 = a paged call met a slot, page id, length or ring state
-    outside its tensor, 5 = a kernel's bounded wait expired)."""
+    outside its tensor, 3 = the status could not be read, or a kernel could not
+    run as built, 5 = a kernel's bounded wait expired; the gravest of them)."""
     return int(lib().wildcat_get_device_status(_stream(stream)))
 
 

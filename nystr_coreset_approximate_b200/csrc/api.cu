@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "../../include/wildcat.h"
+#include "device_status.h"
 #include "internal.h"
 
 using wildcat::Carve;
@@ -348,9 +349,9 @@ int read_device_status(bool clear) {
                          read_paged_status(clear), read_paged_attend_status(clear), read_paged_attend_tc_status(clear)};
     for (const int v : parts)
         if (v < 0) return -1;
-    int worst = 0;  // an expired wait (5) before a bad slot, page id or length (1)
-    for (const int v : parts) worst = v > worst ? v : worst;
-    return worst;
+    int code = 0;
+    for (const int v : parts) code = graver_device_status(code, device_status_code(v));
+    return code;
 }
 }  // namespace wildcat
 
@@ -808,6 +809,7 @@ wildcat_status wildcat_get_device_status(void* stream) {
     if (v == WILDCAT_ERR_TIMEOUT) return record(Status::fail(5, "a kernel's bounded wait expired"));
     if (v == WILDCAT_ERR_INVALID_ARG)
         return record(Status::fail(1, "a kernel met a slot, page id, length or ring state outside its tensor"));
+    if (v != 0) return record(Status::fail(3, "a kernel could not run as built and left its output unwritten"));
     return record(Status::ok());
 }
 
