@@ -612,6 +612,13 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _length(t, name):
+    """The number of entries of a one-dimensional tensor."""
+    if t.dim() != 1:
+        raise ValueError(f"{name} must have one dimension, not the shape {list(t.shape)}")
+    return t.shape[0]
+
+
 def _shape_is(t, name, *shape):
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
@@ -646,7 +653,7 @@ def page_tables(ctx_lens, new_lens, block_table, free_ring, ring_state, page_siz
     requests that did not advance."""
     torch = _torch()
     i32 = torch.int32
-    B = ctx_lens.shape[0]
+    B = _length(ctx_lens, "ctx_lens")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, W]")
     _shape_is(new_lens, "new_lens", B)
@@ -803,7 +810,7 @@ def paged_attend(q, k_pool, v_pool, block_table, seq_lens, cu_new, beta: float, 
     dtype = q.dtype
     if dtype != k_pool.dtype:
         raise TypeError("q and the pools must share a dtype")
-    B = seq_lens.shape[0]
+    B = _length(seq_lens, "seq_lens")
     _shape_is(cu_new, "cu_new", B + 1)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, W]")
