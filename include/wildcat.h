@@ -354,8 +354,8 @@ wildcat_status wildcat_paged_write(const void* k, int64_t k_token, int64_t k_hea
  *   e_i = L - n + i + 1 for token i of a request's n new ones (causal), else L,
  * L = seq_lens[b] (the new tokens counted in when causal, their keys and values
  * already in the cache).  Query head x reads key head x / (Hq / Hkv).  A row that
- * sees no key is zero.  Rows of Q at or past cu_new[B] are not read, and those
- * rows of O not written.  What the cache holds at positions at or past L does not
+ * sees no key is zero.  What rows of Q at or past cu_new[B] hold does not matter,
+ * and those rows of O are not written.  What the cache holds at positions at or past L does not
  * matter (infinities and NaN included); a NaN or infinite key or value at a
  * visible position of one row may reach the rows near it that do not see it.
  * A page id outside the pool reads as zero keys and values, and a length past

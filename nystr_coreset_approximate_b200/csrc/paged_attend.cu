@@ -61,22 +61,27 @@ struct SimtArgs {
     int G;
 };
 
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, bool wide, float (&v)[4]);
-template <>
-__device__ __forceinline__ void load4<float>(const float* p, bool wide, float (&v)[4]) {
+// Four values, widened.  The pools are read through the read-only path (RO); Q is not: O
+// may be Q itself, and what that path reads must not be written while the kernel runs.
+template <bool RO, typename V>
+__device__ __forceinline__ V load_as(const void* p) {
+    if constexpr (RO) return __ldg(static_cast<const V*>(p));
+    else return *static_cast<const V*>(p);
+}
+template <bool RO>
+__device__ __forceinline__ void load4(const float* p, bool wide, float (&v)[4]) {
     if (wide) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+        const float4 a = load_as<RO, float4>(p);
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = __ldg(p + k);
+        for (int k = 0; k < 4; ++k) v[k] = load_as<RO, float>(p + k);
     }
 }
-template <>
-__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, bool wide, float (&v)[4]) {
+template <bool RO>
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, bool wide, float (&v)[4]) {
     if (wide) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        const uint2 u = load_as<RO, uint2>(p);
         v[0] = __uint_as_float(u.x << 16);
         v[1] = __uint_as_float(u.x & 0xffff0000u);
         v[2] = __uint_as_float(u.y << 16);
@@ -120,7 +125,7 @@ struct Rows {
             const int c = (threadIdx.x + i * kThreads) % (D / 4) * 4;
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[i][k] = 0.f;
-            if (id[i] >= 0 && id[i] < a.s.pages) load4<T>(base + (int64_t)id[i] * sp + (int64_t)at[i] * sr + c, a.wide, v[i]);
+            if (id[i] >= 0 && id[i] < a.s.pages) load4<true>(base + (int64_t)id[i] * sp + (int64_t)at[i] * sr + c, a.wide, v[i]);
         }
         if (bad) atomicMax(&g_paged_attend_status, 1);
     }
@@ -147,7 +152,7 @@ __device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* 
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (r < g.rows) {
             const int x = g.row0 + r, i = x / a.s.g;
-            load4<T>(static_cast<const T*>(a.Q) + (int64_t)(first + i) * a.q_t +
+            load4<false>(static_cast<const T*>(a.Q) + (int64_t)(first + i) * a.q_t +
                          (int64_t)(g.h * a.s.g + x - i * a.s.g) * a.q_h + c,
                      a.wide, v);
         }
@@ -319,7 +324,7 @@ __device__ void simt_few(const SimtArgs& a, const Seg& g, float* sm) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) q[r][k] = acc[r][k] = 0.f;
         if (r < g.rows)
-            load4<T>(static_cast<const T*>(a.Q) + (int64_t)(first + i) * a.q_t + (int64_t)(g.h * a.s.g + x - i * a.s.g) * a.q_h + col,
+            load4<false>(static_cast<const T*>(a.Q) + (int64_t)(first + i) * a.q_t + (int64_t)(g.h * a.s.g + x - i * a.s.g) * a.q_h + col,
                      a.wide, q[r]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) q[r][k] *= a.scale;
@@ -344,8 +349,8 @@ __device__ void simt_few(const SimtArgs& a, const Seg& g, float* sm) {
             for (int k = 0; k < 4; ++k) k4[u][k] = v4[u][k] = 0.f;
             if (j < hi) {
                 if (id[u] >= 0 && id[u] < a.s.pages) {
-                    load4<T>(K + (int64_t)id[u] * a.k_p + (int64_t)at * a.k_r, a.wide, k4[u]);
-                    load4<T>(V + (int64_t)id[u] * a.v_p + (int64_t)at * a.v_r, a.wide, v4[u]);
+                    load4<true>(K + (int64_t)id[u] * a.k_p + (int64_t)at * a.k_r, a.wide, k4[u]);
+                    load4<true>(V + (int64_t)id[u] * a.v_p + (int64_t)at * a.v_r, a.wide, v4[u]);
                 } else {
                     bad = true;
                 }

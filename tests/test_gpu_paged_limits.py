@@ -116,3 +116,37 @@ def test_tables_report_lengths_and_rings_out_of_range(ctx, new, ring, head, coun
     (seq, cu, _, slots, state), *_, status, again = _bad_call(ctx, new, [[3, 4], [5, 6]], ring, head, count)
     assert (seq, slots[:cu[-1]], state) == what
     assert (status, again) == (1, 0)
+
+
+# ----------------------------------------------------------- queries that are overwritten or void
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _attend(c, **kw):
+    return wc.paged_attend(kw.pop("q", c["q"]), c["k_pool"], c["v_pool"], c["d_table"], c["d_lens"], c["d_cu"], 0.17, **kw)
+
+
+@pytest.mark.parametrize("dtype,d", [(F32, 32), (BF, 32), (F32, 64), (BF, 64), (F32, 128)], ids=str)
+def test_attend_in_place_where_units_share_cache_lines(dtype, d):
+    """Every key head's unit writes its rows between those that other blocks still read."""
+    new = [1, 40, 1, 3, 70, 2]
+    c = pc.paged_inputs(41, [300, 40, 2, 90, 700, 65], new, 6, 6, d, 16, dtype, nan=False)
+    want = _attend(c)
+    ref, _, A, size = pc.attend_plain(c["q"], c["k_pool"], c["v_pool"], c["table"], c["lens"], c["cu"], 0.17, True)
+    assert (want.double().cpu() - ref).abs().le(pc.attend_bound(ref, A, size, dtype, d, 700)).all()
+    for _ in range(10):
+        q = c["q"].clone()
+        assert _attend(c, q=q, out=q) is q and torch.equal(q, want)
+    assert wc.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=str)
+@pytest.mark.parametrize("void", [float("nan"), float("inf")])
+def test_attend_with_void_queries_behind_the_last_request(dtype, void):
+    """A tile of rows may reach past the last request's; what stands there changes nothing."""
+    c = pc.paged_inputs(42, [33, 150], [5, 30], 4, 2, 64, 16, dtype, extra_rows=100)
+    want = _attend(c, out=torch.zeros_like(c["q"]))
+    c["q"][35:] = void
+    assert torch.equal(_attend(c, out=torch.zeros_like(c["q"])), want)
+    assert (want[35:] == 0).all() and want.isfinite().all()
+    assert wc.device_status() == 0
