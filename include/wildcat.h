@@ -556,7 +556,7 @@ wildcat_status wildcat_pivot_uniforms(uint64_t seed, int64_t BH, int steps, doub
 /*
  * wildcat_get_device_status -- waits for `stream`, then reports and clears
  * the device status words of the current device.  Kernels that wait on
- * mbarriers (the tensor-core weights and attend) or on counters (the select's
+ * mbarriers (the tensor-core weights, attend and paged attention) or on counters (the select's
  * global-sync form) bound
  * every wait by a time limit; when one expires the kernel records
  * WILDCAT_ERR_TIMEOUT there, stops issuing work, waits (bounded) for its
@@ -577,7 +577,9 @@ wildcat_status wildcat_get_device_status(void* stream);
  * nanoseconds > 0 every later tensor-core attend launch first waits that long
  * on a barrier phase that nothing completes, records WILDCAT_ERR_TIMEOUT in
  * the device status word, releases its tensor memory and returns without
- * writing O.  0 turns the hook off.  Process-wide; for tests only.
+ * writing O; of every later wildcat_paged_attend on the tensor cores the first
+ * block gives up so while its copies and products are on their way, and the
+ * rows that it has a part in are not written.  0 turns the hook off.  Process-wide; for tests only.
  * Returns WILDCAT_ERR_INVALID_ARG outside [0, 1e9].
  */
 wildcat_status wildcat_test_force_wait_timeout(int64_t nanoseconds);

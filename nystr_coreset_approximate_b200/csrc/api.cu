@@ -817,6 +817,7 @@ wildcat_status wildcat_test_force_wait_timeout(int64_t nanoseconds) {
     if (nanoseconds < 0 || nanoseconds > 1000000000LL)
         return bad(1, "%s: nanoseconds must be in [0, 1e9]", "wildcat_test_force_wait_timeout");
     wildcat::set_attend_force_timeout((unsigned long long)nanoseconds);
+    wildcat::set_paged_attend_force_timeout((unsigned long long)nanoseconds);
     return record(Status::ok());
 }
 

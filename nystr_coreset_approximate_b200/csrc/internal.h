@@ -250,6 +250,7 @@ Status launch_paged_attend_tc(const PagedAttendRequest& q, cudaStream_t stream);
 int read_paged_status(bool clear);
 int read_paged_attend_status(bool clear);
 int read_paged_attend_tc_status(bool clear);
+void set_paged_attend_force_timeout(unsigned long long ns);
 
 // per-instance key mean (binning.cu), fp64 partial sums then fp32 mean
 size_t key_mean_workspace_bytes(int64_t BH, int64_t n, int d);

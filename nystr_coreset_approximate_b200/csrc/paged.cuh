@@ -23,10 +23,13 @@ namespace wildcat {
 namespace paged {
 
 struct Plan {
-    int4* joins;        // [G] the cut unit that ends in block c: (b, h, t, first block), first block -1 for none
+    int4* joins;        // [G] the cut unit that ends in block c: (b, h, t, first block), first block kNoJoin for none
     float* part;        // [2 G][M][D] partial sums of the exponentials times V
     float2* ml;         // [2 G][M] their maximum (of beta s, in powers of two) and sum
 };
+
+constexpr int kNoJoin = -1;   // no cut unit ends in the block
+constexpr int kGaveUp = -2;   // the block gave up (an expired wait): its pieces may be missing
 
 inline size_t carve_plan(Carve& cv, Plan* p, int G, int M, int D) {
     p->joins = static_cast<int4*>(cv.take(sizeof(int4) * G));

@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     __shared__ ShareScratch scratch;
     find_share<kN>(a.s, a.G, &scratch, &g_paged_attend_status);
     __syncthreads();
-    int4 join = make_int4(0, 0, 0, -1);
+    int4 join = make_int4(0, 0, 0, kNoJoin);
     {
         Walk<kN> w;
         w.start(a.s, scratch.share);

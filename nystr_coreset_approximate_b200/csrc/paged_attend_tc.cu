@@ -41,8 +41,8 @@
 //
 // Every wait is bounded (2 s) and gives up when another role has given up; an
 // expired wait records WILDCAT_ERR_TIMEOUT in the device status word, the block
-// drains its copies and products (bounded), frees its tensor memory and returns.
-// No load uses cluster multicast.
+// drains its copies and products (bounded), marks its pieces as missing, frees its
+// tensor memory and returns.  No load uses cluster multicast.
 //
 // Measured: 2,048 new tokens behind 30,001 (32/8 heads of 128) 0.91 to 1.05 ms, 1.0 to
 // 1.15 PFLOP/s in 1.32 M cycles, under the power cap; one token each of 32 requests of
@@ -89,7 +89,7 @@ struct Bars {
     uint64_t k_full[NK], k_empty[NK], v_full[NV], v_fixed[NV], v_empty[NV];
     uint64_t s_go, s_full[2], p_full[2], pv_done[2], o_full[2], o_free[2], den_full[2];
     uint64_t item_full[kItems], item_empty[kItems];
-    uint64_t drain;
+    uint64_t drain, never;
     unsigned tmem_base;
     int abort;
 };
@@ -127,6 +127,7 @@ struct TcArgs {
     float scale;  // beta log2(e)
     int G, R;     // blocks; rows of a row tile
     int box;      // rows of a page in one copy: min(page_size, 128)
+    unsigned long long stall_ns;  // test hook, 0 = off: warp 2 of block 0 waits this long on `never`
 };
 
 template <int D>
@@ -522,7 +523,7 @@ __device__ __forceinline__ void role_mma(const Ctx<D>& x, const TcArgs& a) {
 
 // Warp 2.
 template <int D>
-__device__ __forceinline__ void role_tail(const Ctx<D>& x, int lane) {
+__device__ __forceinline__ void role_tail(const Ctx<D>& x, const TcArgs& a, int lane) {
     using C = Cfg<D>;
     Ring<C::NV> r;
     bool ok = true;
@@ -532,6 +533,10 @@ __device__ __forceinline__ void role_tail(const Ctx<D>& x, int lane) {
         const int t0 = x.item(s)->t0, t1 = x.item(s)->t1, L = x.item(s)->L;
         x.item_done(s, lane);
         if (t0 == t1) break;
+        if (a.stall_ns && s == 0 && blockIdx.x == 0) {  // copies and products of other roles are on their way
+            ok = __all_sync(0xffffffffu, mbar_wait(&x.bars->never, 0, a.stall_ns));
+            if (!ok) break;
+        }
         for (int kt = t0; kt < t1; ++kt, r.next()) {
             ok = x.wait(&x.bars->v_full[r.s], r.ph);
             if (!ok) break;
@@ -773,7 +778,7 @@ __device__ __forceinline__ void role_epilogue(const Ctx<D>& x, const TcArgs& a, 
     unsigned on[2] = {0, 0};
     unsigned k0 = 0;
     bool ok = true;
-    int4 join = make_int4(0, 0, 0, -1);
+    int4 join = make_int4(0, 0, 0, kNoJoin);
     for (unsigned s = 0; ok; ++s) {
         ok = x.item_wait(s);
         if (!ok) break;
@@ -788,7 +793,7 @@ __device__ __forceinline__ void role_epilogue(const Ctx<D>& x, const TcArgs& a, 
         if (g.join >= 0) join = make_int4(g.b, g.h, g.t, g.join);
     }
     if (!ok && lane == 0) x.give_up();
-    if (quad == 0 && lane == 0) a.p.joins[blockIdx.x] = join;
+    if (quad == 0 && lane == 0) a.p.joins[blockIdx.x] = ok ? join : make_int4(0, 0, 0, kGaveUp);
 }
 
 template <int D>
@@ -831,6 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&bars->s_go, 4);  // the warps that took the scores
         mbar_init(&bars->drain, 1);
+        mbar_init(&bars->never, 1);
         // the operand layouts need a 1024-byte aligned base
         bars->abort = (x.sbase & 1023u) ? 1 : 0;
         if (x.sbase & 1023u) atomicMax(&g_paged_tc_status, 3);
@@ -862,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) role_mma<D>(x, a);
                 __syncwarp();
             }
-            else if (warp == 2) role_tail<D>(x, lane);
+            else if (warp == 2) role_tail<D>(x, a, lane);
             else role_copy<D, true>(x, a, &tmQ, &tmV, lane, share);
         }
         __syncwarp();
@@ -872,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsEpilogue));
         if (go) role_epilogue<D>(x, a, warp & 3, lane);
-        else if (warp == 12 && lane == 0) a.p.joins[blockIdx.x] = make_int4(0, 0, 0, -1);
+        else if (warp == 12 && lane == 0) a.p.joins[blockIdx.x] = make_int4(0, 0, 0, kGaveUp);
     }
 
     tc_fence_before();
@@ -883,6 +889,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
     }
 }
+
+std::atomic<unsigned long long> g_stall_ns{0};  // test hook
 
 int sm_count() {
     int dev = 0, n = 0;
@@ -911,6 +919,7 @@ Status run_tc(const PagedAttendRequest& q, cudaStream_t st) {
     a.G = G;
     a.R = R;
     a.box = std::min(q.page_size, kKeys);
+    a.stall_ns = g_stall_ns.load(std::memory_order_relaxed);
     CUtensorMap tmQ, tmK, tmV;
     const uint64_t Du = D, ps = (uint64_t)q.page_size, H = (uint64_t)q.Hkv, P = (uint64_t)q.pages;
     const uint32_t box = (uint32_t)a.box;
@@ -956,6 +965,8 @@ bool paged_attend_tc_supported(const PagedAttendRequest& q) {
 Status launch_paged_attend_tc(const PagedAttendRequest& q, cudaStream_t st) {
     return q.d == 64 ? run_tc<64>(q, st) : run_tc<128>(q, st);
 }
+
+void set_paged_attend_force_timeout(unsigned long long ns) { g_stall_ns.store(ns, std::memory_order_relaxed); }
 
 int read_paged_attend_tc_status(bool clear) {
     int v = 0;

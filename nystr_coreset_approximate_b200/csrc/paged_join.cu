@@ -9,7 +9,8 @@
 // 1 .. c the others (slot 0).  At most one unit ends so in each block.  A warp
 // takes a row or two.  Bounded by the latency of its reads, one after the other
 // (the unit, its rows, the pieces' sums, the pieces, which are in L2): with eight
-// rows to a warp it took 20 us for 148 units of 256 rows.
+// rows to a warp it took 20 us for 148 units of 256 rows.  A unit of which a block
+// gave up is not joined: what that block left in the workspace is not its piece.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.cuh"
@@ -28,7 +29,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedJoin a, i
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x;
     const int4 j = a.p.joins[c];
-    if (j.w < 0) return;
+    if (j.w < 0) return;  // kNoJoin or kGaveUp
     const int c0 = j.w, pieces = c - c0 + 1;
     const int n = a.s.new_tokens(j.x), first = a.s.first_row(j.x);
     const int64_t row0 = (int64_t)j.z * a.s.M;
@@ -38,11 +39,14 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedJoin a, i
     for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < rows; r += gridDim.y * (kJoinThreads / 32)) {
         float m = -INFINITY;
         float2 mine = make_float2(-INFINITY, 0.f);  // of piece `lane`
+        bool lost = false;
         for (int k = lane; k < pieces; k += 32) {
             const float2 ml = a.p.ml[((int64_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * M + r];
+            lost = lost || a.p.joins[c0 + k].w == kGaveUp;
             if (k < 32) mine = ml;
             m = fmaxf(m, ml.x);
         }
+        if (__any_sync(0xffffffffu, lost)) return;
         m = warp_max(m);
         const float base = m == -INFINITY ? 0.f : m;
         float l = 0.f, acc[W];

@@ -150,3 +150,32 @@ def test_attend_with_void_queries_behind_the_last_request(dtype, void):
     assert torch.equal(_attend(c, out=torch.zeros_like(c["q"])), want)
     assert (want[35:] == 0).all() and want.isfinite().all()
     assert wc.device_status() == 0
+
+
+# ------------------------------------------------------------------------- waits that run out
+@pytest.mark.parametrize("lens,new,Hq,Hkv,d", [
+    ([60001, 20], [1, 1], 4, 2, 64),  # one key head's row cut into pieces over many blocks
+    ([3000, 500], [500, 1], 8, 1, 128),  # units of two row tiles
+    ([130] * 600, [1] * 600, 2, 1, 64),  # whole units in every block
+], ids=["long", "chunk", "short"])
+def test_a_block_that_gives_up_is_told_and_spoils_no_other(lens, new, Hq, Hkv, d):
+    """The hook lets a wait of the first block run out after 1 ms, its copies and products on their way.  The rows that it
+    has a part in stay as they were (no piece of it is joined), all others are as always, and so is the next call."""
+    c = pc.paged_inputs(43, lens, new, Hq, Hkv, d, 16, BF, nan=False)
+    want_lse, lse = (torch.full(c["q"].shape[:2], 3.25, device="cuda") for _ in range(2))
+    want = _attend(c, lse=want_lse)
+    assert wc.device_status() == 0
+    assert wc.lib().wildcat_test_force_wait_timeout(1_000_000) == 0
+    try:
+        out = _attend(c, out=torch.full_like(c["q"], 3.25), lse=lse)
+        assert wc.device_status() == 5
+    finally:
+        assert wc.lib().wildcat_test_force_wait_timeout(0) == 0
+    untouched = (out == 3.25).all(-1)
+    assert torch.equal(untouched, lse == 3.25)
+    assert torch.equal(out[~untouched], want[~untouched]) and torch.equal(lse[~untouched], want_lse[~untouched])
+    # the first units of the line, and no more than a block's share of them
+    units = untouched.view(-1, Hkv, Hq // Hkv).all(-1)
+    assert units[0, 0] and units.sum() <= {"60001": 1, "3000": 32, "130": 5}[str(lens[0])]
+    again = _attend(c, lse=lse)
+    assert torch.equal(again, want) and torch.equal(lse, want_lse) and wc.device_status() == 0
