@@ -370,8 +370,9 @@ wildcat_status wildcat_paged_write(const void* k, int64_t k_token, int64_t k_hea
  *          be Q itself with the same strides
  *   lse    out [T, Hq] float32 log of the sum of exponentials (-inf for rows that
  *          see no key), or NULL
- *   workspace >= wildcat_paged_attend_workspace_size(B, d) bytes; two calls that
- *          may run at the same time need two of them
+ *   workspace >= wildcat_paged_attend_workspace_size(B, d) bytes (two pieces for
+ *          every SM, whatever B is: 39 MB at d = 128); two calls that may run at the
+ *          same time need two of them
  */
 size_t wildcat_paged_attend_workspace_size(int64_t B, int d);
 wildcat_status wildcat_paged_attend(const void* Q, int64_t q_token, int64_t q_head,

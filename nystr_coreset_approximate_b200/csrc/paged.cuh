@@ -10,8 +10,8 @@
 // there.  Every block so has about the same work whatever the lengths
 // are: one long request is spread over the GPU, and many short ones are packed.
 // A unit that lies whole in one block is finished there; of one that is cut, each
-// block leaves a partial sum, and join_kernel joins them in the order of the keys,
-// the same in every run.  Each block finds its place in the line for itself.
+// block leaves a partial sum, and paged_join_kernel joins them in the order of the
+// keys, the same in every run.  Each block finds its place in the line for itself.
 #pragma once
 
 #include <atomic>
@@ -67,7 +67,7 @@ struct Shape {
         return (int)min(max((int64_t)cu_new[b], (int64_t)0), T);
     }
     __device__ __forceinline__ int new_tokens(int b) const { return max(first_row(b + 1) - first_row(b), 0); }
-    // a length past the table's pages is cut to them (and reported by the plan); so is one
+    // a length past the table's pages is cut to them (find_share reports it); so is one
     // whose last key tile would end past 2^31
     __device__ __forceinline__ int64_t most() const { return min(W * page_size, (int64_t)0x7fffff00); }
     __device__ __forceinline__ int length(int b) const { return (int)min((int64_t)max(seq_lens[b], 0), most()); }
@@ -161,8 +161,10 @@ struct Seg {
     int64_t first_end;           // the last place of the unit's first key tile
 };
 
-// The T places in all and the blocks that share them.  Each of several has enough places
-// for a key tile to end in it.
+// The T places in all and the blocks that share them.  Each block has at least the 2^wide
+// places of a key tile, so that one that lies wholly within a unit's key tiles finishes
+// one: the join takes a piece from every block between the first piece's and the last's.
+// (Where a unit begins, a block may have no more than its kUnitCost places, and no piece.)
 struct Line {
     int64_t total, each;  // places of a block, and one more for the first `rest` of them
     int active, rest;

@@ -30,3 +30,12 @@ def test_the_message_names_the_lengths():
         wc.page_tables(wide, torch.zeros(2, **I32), table, wide, wide, 16, 4)
     with pytest.raises(ValueError, match="seq_lens must have one dimension"):
         wc.paged_attend(torch.zeros(5, 2, 64), *[torch.zeros(3, 2, 16, 64)] * 2, table, wide, torch.zeros(3, **I32), 0.1)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_the_workspace_does_not_depend_on_the_requests(d):
+    """It holds two pieces of 256 rows for each of 148 SMs (148 where no GPU is there to ask) with a maximum and a sum for each
+    row, a join for each, and the padding of three parts."""
+    sizes = {int(wc.lib().wildcat_paged_attend_workspace_size(B, d)) for B in (0, 1, 1000, 65535)}
+    pieces = 2 * 148 * 256 * (d + 2) * 4
+    assert len(sizes) == 1 and (torch.cuda.is_available() or pieces <= sizes.pop() <= pieces + 148 * 16 + 1024)
