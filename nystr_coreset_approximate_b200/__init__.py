@@ -721,13 +721,17 @@ def rotary(x, positions, inv_freq, sections, *, interleaved: bool = False, out=N
     float64 radians per position; sections: the pairs of each axis, summing to
     h <= d / 2.  Pair i is elements (i, i + h), or (2 i, 2 i + 1) when
     interleaved; elements past 2 h are copied.  For Q or K [BH, n, d] with one
-    grid of positions, pass Q.transpose(0, 1).  out may be x itself."""
+    grid of positions, pass Q.transpose(0, 1).  out may be x itself.
+
+    As all calls here it records no gradient: the result of an x that requires
+    one is detached from it.  A program that trains calls rotary_backward in
+    its own backward pass (torch.autograd.Function)."""
     return _rotary(x, positions, inv_freq, sections, interleaved, 0, out, stream, "x")
 
 
 def rotary_backward(grad_out, positions, inv_freq, sections, *, interleaved: bool = False, out=None, stream=None):
     """The gradient of rotary's x from that of its result: the turn by minus
-    the angle."""
+    the angle, with rotary's other arguments (and recorded no more than it)."""
     return _rotary(grad_out, positions, inv_freq, sections, interleaved, 1, out, stream, "grad_out")
 
 

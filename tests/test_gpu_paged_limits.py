@@ -179,3 +179,47 @@ def test_a_block_that_gives_up_is_told_and_spoils_no_other(lens, new, Hq, Hkv, d
     assert units[0, 0] and units.sum() <= {"60001": 1, "3000": 32, "130": 5}[str(lens[0])]
     again = _attend(c, lse=lse)
     assert torch.equal(again, want) and torch.equal(lse, want_lse) and wc.device_status() == 0
+
+
+# ------------------------------------------------------------------- turning queries and gradients
+@pytest.mark.parametrize("dtype", [F32, BF], ids=str)
+@pytest.mark.parametrize("d,half", [(64, 32), (34, 14)], ids=str)  # 16 bytes a load, and element by element
+def test_write_turns_queries_in_their_place(dtype, d, half):
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    T, Hq, Hkv, page = 45, 6, 2, 8
+    qkv = torch.randn(T, Hq + 2 * Hkv, d, generator=gen, device="cuda").to(dtype)
+    slots = torch.randperm(8 * page, generator=gen, device="cuda")[:T].to(torch.int32)
+    slots[7] = -1  # not written, but its queries are turned
+    pos = torch.randint(0, 9000, (2, T), generator=gen, device="cuda").to(torch.int32)
+    turn = dict(positions=pos, inv_freq=torch.rand(half, generator=gen, device="cuda", dtype=torch.float64), sections=(half - 5, 5))
+    pools = [torch.zeros(8, Hkv, page, d, dtype=dtype, device="cuda") for _ in range(4)]
+    q, k, v = qkv.split([Hq, Hkv, Hkv], 1)
+    want = wc.paged_write(k, v, slots, *pools[:2], q=q, **turn)
+    rest = qkv[:, Hq:].clone()
+    assert wc.paged_write(k, v, slots, *pools[2:], q=q, out=q, **turn) is q
+    assert torch.equal(q, want) and torch.equal(qkv[:, Hq:], rest)
+    assert torch.equal(pools[2], pools[0]) and torch.equal(pools[3], pools[1])
+    assert wc.device_status() == 0
+
+
+def test_rotary_and_its_backward_in_an_autograd_function():
+    """What the documentation tells a program that trains to do."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(9, 3, 32, generator=gen, device="cuda", requires_grad=True)
+    dy = torch.randn(9, 3, 32, generator=gen, device="cuda")
+    pos = torch.randint(0, 500, (1, 9), generator=gen, device="cuda").to(torch.int32)
+    freq = torch.rand(16, generator=gen, device="cuda", dtype=torch.float64)
+
+    class Turn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return wc.rotary(x, pos, freq, (16,))
+
+        @staticmethod
+        def backward(ctx, dy):
+            return wc.rotary_backward(dy, pos, freq, (16,))
+
+    assert not wc.rotary(x, pos, freq, (16,)).requires_grad
+    (grad,) = torch.autograd.grad((Turn.apply(x) * dy).sum(), x)
+    ref, size = pc.rotary_plain(dy, pos, freq, (16,), back=True)
+    assert (grad.double().cpu() - ref).abs().le(pc.rotary_bound(ref, size, F32)).all()
