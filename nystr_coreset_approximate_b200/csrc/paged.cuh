@@ -73,6 +73,9 @@ struct Shape {
     __device__ __forceinline__ int length(int b) const { return (int)min((int64_t)max(seq_lens[b], 0), most()); }
 };
 
+// With 1, 2 and 4 (us, bf16): 2,000 decoded tokens over one key tile 586, 600, 597, over
+// two 717, 748, 750; 64 over 900 keys 79, 80, 80, three of them 17.3, 17.0, 16.0; 16 prompts
+// of 300 tokens 62.7, 63.9, 61.0; 200 tokens over 600 keys with heads of 64 275, 267, 259.
 constexpr int kUnitCost = 2;
 
 // x / y of what nearly always fits in 32 bits: a division of 64 bits takes some hundred

@@ -10,14 +10,18 @@
 //
 // Here: the dispatch, and the CUDA-core kernel, for
 // float32 and for bf16 in shapes that the tensor cores' copies do not take
-// (d = 32, a page that is no multiple of 8 rows, strides that are no multiple
-// of 16 bytes).  It works in float32 throughout: one row tile is 64 rows, or 16
-// where the unit has no more, against 64 keys (units of up to four rows go without
-// tiles); a thread holds 4 x 4 (1 x 4) scores and 4 (1) rows of D / 16 accumulators, in packed pairs.  A
-// tile of 64 rows takes 8,000 cycles of an SM that has two blocks (4,096 of them
-// multiply-adds, 3,000 reads of shared memory): 900 new tokens of two requests in
-// 154 us at d = 128 (22 TFLOP/s); 32 decoded ones over 4,000 keys in 137 us (2.9
-// TB/s; 300 us in tiles).
+// (d = 32, pages that neither divide 128 rows in whole groups of 8 nor are a
+// multiple of 128, strides that are no multiple of 16 bytes).  It works in float32
+// throughout: one row tile is 64 rows, or 16 where the unit has no more, against
+// 64 keys (units of up to four rows go without tiles); a thread holds 4 x 4 (1 x 4)
+// scores and 4 (1) rows of D / 16 accumulators, in packed pairs.  A tile of 64 rows
+// takes 8,000 cycles of an SM that has two blocks (4,096 of them multiply-adds,
+// 3,000 reads of shared memory).  In float32, two requests of 2,000 tokens, 900 of
+// them new, with 8/2 heads of 128: 405 us (28 TFLOP/s); 32 decoded tokens over 4,000
+// keys each, 8 key heads of 128 with one query head 299 us (3.5 TB/s), with four 385,
+// with five to sixteen 747 (1.4 TB/s, in tiles).  bf16 there: 32 over 4,000 with
+// 32/8 heads of 32 166 us (0.8 TB/s), with heads of 128 in pages of 48 rows 654 us,
+// where the tensor cores take 102 with pages of 16.
 #include <algorithm>
 #include <cfloat>
 
@@ -306,6 +310,10 @@ __device__ void simt_segment(const SimtArgs& a, const Seg& g, float* Qs, float* 
 // (11,600 cycles for 64 keys).  D / 4 lanes make a stream that takes every kStreams-th
 // key, straight from memory to registers, four keys at a time, with a running maximum,
 // sum and accumulators of its own; the streams are joined in shared memory, in order.
+// Why four: 32 x 4,000 keys, 8 key heads of 64, float32, take 155, 167, 181, 195 us with
+// one to four rows, and 404 in tiles with any number.  A build for up to eight rows
+// takes 276, 301, 328, 366 with five to eight, but 179 to 252 with one to four: its
+// registers cost the common cases a sixth to a third.
 constexpr int kFew = 4;
 template <typename E, int D>
 __device__ void simt_few(const SimtArgs& a, const Seg& g, float* sm) {
