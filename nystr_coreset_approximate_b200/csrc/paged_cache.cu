@@ -283,6 +283,16 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[VEC
     }
 }
 
+// The pair (a, b) turned by (cos, sin).  Which product is rounded on its own is said here
+// and not left to the compiler, so that the loads' width (the strides and alignment of any
+// tensor of the call) does not change a result.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn_pair(float& a, float& b, float2 cs) {
+    const float u = fmaf(a, cs.x, -__fmul_rn(b, cs.y));
+    b = INTERLEAVED ? fmaf(b, cs.x, __fmul_rn(a, cs.y)) : fmaf(a, cs.y, __fmul_rn(b, cs.x));
+    a = u;
+}
+
 // One block: `tokens_per_block` tokens, all heads of all parts.  Work comes in
 // units of 2 VEC elements of one head: VEC pairs where the part is rotated
 // (elements c and c + half, or 2 VEC neighbours for interleaved pairs), else
@@ -352,24 +362,14 @@ __global__ void __launch_bounds__(kTurnThreads) turn_kernel(TurnRequest q, int t
             const float2* cs = turn_sm + tt * half + c * VEC;
             if (!q.interleaved) {
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    const float a = x[k], b = y[k];
-                    x[k] = a * cs[k].x - b * cs[k].y;
-                    y[k] = b * cs[k].x + a * cs[k].y;
-                }
+                for (int k = 0; k < VEC; ++k) turn_pair<false>(x[k], y[k], cs[k]);
             } else if constexpr (VEC == 1) {
-                const float a = x[0], b = y[0];
-                x[0] = a * cs[0].x - b * cs[0].y;
-                y[0] = b * cs[0].x + a * cs[0].y;
+                turn_pair<true>(x[0], y[0], cs[0]);
             } else {
 #pragma unroll
                 for (int k = 0; k < VEC / 2; ++k) {
-                    const float a = x[2 * k], b = x[2 * k + 1], e = y[2 * k], f = y[2 * k + 1];
-                    const float2 c0 = cs[k], c1 = cs[VEC / 2 + k];
-                    x[2 * k] = a * c0.x - b * c0.y;
-                    x[2 * k + 1] = b * c0.x + a * c0.y;
-                    y[2 * k] = e * c1.x - f * c1.y;
-                    y[2 * k + 1] = f * c1.x + e * c1.y;
+                    turn_pair<true>(x[2 * k], x[2 * k + 1], cs[k]);
+                    turn_pair<true>(y[2 * k], y[2 * k + 1], cs[VEC / 2 + k]);
                 }
             }
         }

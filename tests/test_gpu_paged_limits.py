@@ -223,3 +223,26 @@ def test_rotary_and_its_backward_in_an_autograd_function():
     (grad,) = torch.autograd.grad((Turn.apply(x) * dy).sum(), x)
     ref, size = pc.rotary_plain(dy, pos, freq, (16,), back=True)
     assert (grad.double().cpu() - ref).abs().le(pc.rotary_bound(ref, size, F32)).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=str)
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_turned_values_do_not_depend_on_the_layout(dtype, interleaved):
+    """The same rows in tensors that take 16 bytes a load and in tensors that do not, alone and beside a pool that does
+    not: bit for bit the same."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    T, H, d, half = 200, 3, 128, 64
+    x = torch.randn(T, H, d, generator=gen, device="cuda").to(dtype)
+    odd = torch.zeros(T, H, d + 1, dtype=dtype, device="cuda")[..., 1:].copy_(x)
+    pos = torch.randint(0, 100000, (2, T), generator=gen, device="cuda").to(torch.int32)
+    turn = dict(positions=pos, inv_freq=torch.rand(half, generator=gen, device="cuda", dtype=torch.float64), sections=(40, 24),
+                interleaved=interleaved)
+    want = wc.rotary(x, **turn)
+    assert torch.equal(wc.rotary(odd, **turn), want)
+    assert torch.equal(wc.rotary_backward(odd, **turn), wc.rotary_backward(x, **turn))
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    for wide in (0, 1):
+        pools = [torch.zeros(T // 8, H, 8, d + wide, dtype=dtype, device="cuda")[..., wide:] for _ in range(2)]
+        assert torch.equal(wc.paged_write(x, x, slots, *pools, q=x, **turn), want)
+        assert torch.equal(pools[0].transpose(1, 2).reshape(T, H, d), want)
+        assert torch.equal(pools[1].transpose(1, 2).reshape(T, H, d), x)
