@@ -284,7 +284,9 @@ wildcat_status wildcat_decode_attend(const void* Q_new, const void* K_new, const
  *                and come back (the pool's, or a part of them)
  *   ring_state   [2] int32: place of the first free page in the ring, free pages
  *   seq_lens     out [B] int32 lengths after the step (0 for a request that ends)
- *   cu_new       out [B + 1] int32 new tokens before each request
+ *   cu_new       out [B + 1] int32 new tokens before each request, those of requests
+ *                that do not advance (or have no room in max_tokens) among them: what
+ *                wildcat_paged_attend gives for their rows means nothing
  *   positions, slots  out [max_tokens] int32; rows behind the last token get
  *                position 0 and slot -1
  *   ring_out     out [4] int32: the ring's state after the step (2 entries),
@@ -358,9 +360,10 @@ wildcat_status wildcat_paged_write(const void* k, int64_t k_token, int64_t k_hea
  * and those rows of O are not written.  What the cache holds at positions at or past L does not
  * matter (infinities and NaN included); a NaN or infinite key or value at a
  * visible position of one row may reach the rows near it that do not see it.
- * A page id outside the pool reads as zero keys and values, and a length past
- * W * page_size is cut to it; both leave WILDCAT_ERR_INVALID_ARG in the device
- * status.
+ * A page id outside the pool reads as zero keys and values, a length past
+ * W * page_size is cut to it, one below zero counts as zero, and entries of
+ * cu_new are cut to 0 .. T (a request whose entries fall has no new tokens); each
+ * leaves WILDCAT_ERR_INVALID_ARG in the device status.
  *
  *   Q      [T, Hq, d], dtype `dtype`, element strides q_token and q_head
  *   k_pool, v_pool  [pages, Hkv, page_size, d], HOST strides {page, head, row}

@@ -9,7 +9,7 @@
 //   numbers, and every value has one writer, so results do not depend on any
 //   order.  The kernel is latency: three prefix sums over the requests, which
 //   every block forms for itself (no block waits for another), then each block
-//   writes its share of tokens and pages.  5.9 us for 64 requests, 8.8 us for 1,000
+//   writes its share of tokens and pages.  6.0 us for 64 requests, 8.8 us for 1,000
 //   with 90 prompts (graph replays); a call costs the host 14 us.
 // turn_kernel  rotary positions with several axes, and the cache writes fused
 //   with them: pair i of axis a turns by the angle p_a f_i,

@@ -246,3 +246,23 @@ def test_turned_values_do_not_depend_on_the_layout(dtype, interleaved):
         assert torch.equal(wc.paged_write(x, x, slots, *pools, q=x, **turn), want)
         assert torch.equal(pools[0].transpose(1, 2).reshape(T, H, d), want)
         assert torch.equal(pools[1].transpose(1, 2).reshape(T, H, d), x)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=str)
+@pytest.mark.parametrize("cu", [[0, 2, 9], [-3, 2, 4], [0, 2, 2 ** 31 - 1], [-(2 ** 31), 2, 4]], ids=str)
+def test_attend_cuts_rows_to_the_queries(dtype, cu):
+    """Rows of new tokens that no query stands for: the others as if they were not there, and the device status says so."""
+    c = pc.paged_inputs(44, [50, 90], [2, 2], 4, 2, 64, 16, dtype)
+    want = _attend(c)
+    assert wc.device_status() == 0
+    assert torch.equal(_attend(dict(c, d_cu=_i32(cu))), want)
+    assert wc.device_status() == 1 and wc.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=str)
+def test_attend_negative_lengths_are_empty(dtype):
+    c = pc.paged_inputs(45, [0, 90], [1, 2], 4, 2, 64, 16, dtype)
+    want = _attend(c)
+    assert wc.device_status() == 0
+    assert torch.equal(_attend(dict(c, d_lens=_i32([-7, 90]))), want) and (want[0] == 0).all()
+    assert wc.device_status() == 1 and wc.device_status() == 0
