@@ -217,9 +217,9 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesRequest 
         q.positions[t] = pos;
         q.slots[t] = slot;
     }
-    // pages handed out
-    for (int k = at; k < min(first[B], count); k += stride) {
-        const int b = range_of(first, B, k);
+    // pages handed out (64 bits: the step past the last of up to 2^31 - 1 of them)
+    for (int64_t k = at; k < min(first[B], count); k += stride) {
+        const int b = range_of(first, B, (int)k);
         const int64_t ctx = max(q.ctx_lens[b], 0);
         if (first[b + 1] > count) continue;
         const int64_t have = (ctx + page - 1) / page;
@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesRequest 
         q.table[b * q.table_stride + have + (k - first[b])] = id;
     }
     // pages given back: never onto the entries read above (those are the ring's filled part)
-    for (int k = at; k < min(gfirst[B], P - count); k += stride) {
-        const int b = range_of(gfirst, B, k);
+    for (int64_t k = at; k < min(gfirst[B], P - count); k += stride) {
+        const int b = range_of(gfirst, B, (int)k);
         const int id = q.table[b * q.table_stride + (k - gfirst[b])];
         bad = bad || no_page(id);
         q.ring[((int64_t)head + count + k) % P] = id;

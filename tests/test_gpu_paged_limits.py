@@ -266,3 +266,18 @@ def test_attend_negative_lengths_are_empty(dtype):
     assert wc.device_status() == 0
     assert torch.equal(_attend(dict(c, d_lens=_i32([-7, 90]))), want) and (want[0] == 0).all()
     assert wc.device_status() == 1 and wc.device_status() == 0
+
+
+def test_tables_of_as_many_pages_as_32_bits_hold():
+    """One request of 2^31 - 1 pages ends (a table and a ring of 8.6 GB each)."""
+    n = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of free memory")
+    table = torch.arange(n, dtype=torch.int32, device="cuda").flip(0)[None]
+    ring = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    seq, cu, _, slots, state = wc.page_tables(_i32([n]), _i32([-1]), table, ring, _i32([n - 5, 0]), 1, 148 * 512)
+    assert (seq.tolist(), cu.tolist(), state.tolist()) == ([0], [0, 0], [n - 5, n, 0, 0]) and (slots == -1).all()
+    assert torch.equal(ring[-5:], table[0, :5]) and torch.equal(ring[:-5], table[0, 5:])
+    assert wc.device_status() == 0
+    del table, ring, slots
+    torch.cuda.empty_cache()
