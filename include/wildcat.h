@@ -357,9 +357,10 @@ wildcat_status wildcat_paged_write(const void* k, int64_t k_token, int64_t k_hea
  * L = seq_lens[b] (the new tokens counted in when causal, their keys and values
  * already in the cache).  Query head x reads key head x / (Hq / Hkv).  A row that
  * sees no key is zero.  What rows of Q at or past cu_new[B] hold does not matter,
- * and those rows of O are not written.  What the cache holds at positions at or past L does not
- * matter (infinities and NaN included); a NaN or infinite key or value at a
- * visible position of one row may reach the rows near it that do not see it.
+ * and those rows of O are not written.  What the cache holds at positions at or
+ * past L does not matter (infinities and NaN included); a NaN or infinite key or
+ * value at a visible position of one row may reach the rows near it that do not
+ * see it.
  * A page id outside the pool reads as zero keys and values, a length past
  * W * page_size is cut to it, one below zero counts as zero, and entries of
  * cu_new are cut to 0 .. T (a request whose entries fall has no new tokens); each
@@ -560,19 +561,18 @@ wildcat_status wildcat_pivot_uniforms(uint64_t seed, int64_t BH, int steps, doub
 /*
  * wildcat_get_device_status -- waits for `stream`, then reports and clears
  * the device status words of the current device.  Kernels that wait on
- * mbarriers (the tensor-core weights, attend and paged attention) or on counters (the select's
- * global-sync form) bound
- * every wait by a time limit; when one expires the kernel records
- * WILDCAT_ERR_TIMEOUT there, stops issuing work, waits (bounded) for its
- * copies in flight, releases its tensor memory and returns, leaving its
- * output incomplete (the select stops every CTA of the instance at the same
- * step and reports the steps taken as the rank).
+ * mbarriers (the tensor-core weights, attend and paged attention) or on
+ * counters (the select's global-sync form) bound every wait by a time limit;
+ * when one expires the kernel records WILDCAT_ERR_TIMEOUT there, stops issuing
+ * work, waits (bounded) for its copies in flight, releases its tensor memory
+ * and returns, leaving its output incomplete (the select stops every CTA of
+ * the instance at the same step and reports the steps taken as the rank).
  * The paged calls record WILDCAT_ERR_INVALID_ARG there for slots, page ids,
- * lengths and ring states in device memory that lie outside their tensors (such
- * accesses are skipped).  Returns WILDCAT_OK, WILDCAT_ERR_TIMEOUT, WILDCAT_ERR_INVALID_ARG, or
- * WILDCAT_ERR_CUDA if the stream or the status word could not be read, or if a
- * kernel could not run as built and left its output unwritten.  Where several
- * apply: an expired wait first, bad data last.
+ * lengths and ring states in device memory that lie outside their tensors
+ * (such accesses are skipped).  Returns WILDCAT_OK, WILDCAT_ERR_TIMEOUT,
+ * WILDCAT_ERR_INVALID_ARG, or WILDCAT_ERR_CUDA if the stream or the status word
+ * could not be read, or if a kernel could not run as built and left its output
+ * unwritten.  Where several apply: an expired wait first, bad data last.
  */
 wildcat_status wildcat_get_device_status(void* stream);
 
@@ -583,7 +583,8 @@ wildcat_status wildcat_get_device_status(void* stream);
  * the device status word, releases its tensor memory and returns without
  * writing O; of every later wildcat_paged_attend on the tensor cores the first
  * block gives up so while its copies and products are on their way, and the
- * rows that it has a part in are not written.  0 turns the hook off.  Process-wide; for tests only.
+ * rows that it has a part in are not written.  0 turns the hook off.
+ * Process-wide; for tests only.
  * Returns WILDCAT_ERR_INVALID_ARG outside [0, 1e9].
  */
 wildcat_status wildcat_test_force_wait_timeout(int64_t nanoseconds);
